@@ -401,6 +401,171 @@ tern_status tern_gemm_a8(const int8_t* q, int64_t m, int64_t k, int64_t ldq, con
                          const float* bias, tern_act act, int64_t act_from, void* y_bf16,
                          int64_t ldy, void* stream);
 
+/*
+ * The transformer block around the layer.  The pages convert the linear layers
+ * of diffusion transformers ("1.58-bit FLUX", section 1; TerDiT, abstract);
+ * the calls below are the operators that stand between those layers in a
+ * text-conditioned block: attention to an encoder's states, the norms with
+ * the gate and modulation of the block's boundaries, and rotary positions.
+ * The pages give no formula for them; each call states its own.
+ */
+
+/*
+ * A view of per-head vectors: element c of head h of token t of sample b is
+ * data[b * batch + t * token + h * head + c] (strides in elements; the
+ * channels of a head are consecutive).  A [batch, tokens, heads, width] tensor,
+ * a slice of a fused projection and a [batch, heads, tokens, width] tensor are
+ * all such views.  Strides are not negative; an input's may be 0 (a broadcast).
+ */
+typedef struct {
+  void* data;
+  int64_t batch;
+  int64_t token;
+  int64_t head;
+} tern_heads;
+
+/* Which channels of a head make a pair: 2p and 2p + 1, or p and p + P. */
+typedef enum { TERN_ROPE_INTERLEAVED = 0, TERN_ROPE_HALVES = 1 } tern_rope_layout;
+
+#define TERN_ROPE_MAX_AXES 4
+#define TERN_ROPE_MAX_PAIRS 128
+
+/*
+ * Axes of a rotary embedding: axis a takes width[a] channels (even, >= 0) of the
+ * sum 2P <= min(d, 2 TERN_ROPE_MAX_PAIRS); frequencies theta^(-2i / width[a]),
+ * i = 0 .. width[a]/2 - 1.
+ */
+typedef struct {
+  int32_t count; /* 1 .. TERN_ROPE_MAX_AXES */
+  int32_t width[TERN_ROPE_MAX_AXES];
+  double theta; /* > 0, finite */
+  tern_rope_layout layout;
+} tern_rope_axes;
+
+/*
+ * tern_rope: rotary positions with several axes (time, height, width, ...).
+ *
+ * The P pairs of a head are numbered axis by axis; pair number p, the i-th of
+ * axis a, is (u, v) = channels (2p, 2p + 1) or (p, p + P) by axes->layout, and
+ *   angle = pos[b][t][a] * theta^(-2i / width[a])   (negated with inverse != 0)
+ *   (u, v) -> (u cos(angle) - v sin(angle), u sin(angle) + v cos(angle))
+ * in fp32 with one rounding to the output's type; the angle is exact to about
+ * 2^-24 of a turn for |pos| < 2^24.  Channels from 2P on are copied.  The
+ * inverse is the transpose: the gradient of x from the gradient of y.
+ *
+ *   x, y   [b, t, h, d] fp32 or bf16 (dtype); y may be the same view as x,
+ *          otherwise they must not overlap
+ *   pos    fp32 positions: axis a of token t of sample b is
+ *          pos[b * pos_batch + t * pos_token + a] (pos_batch = 0: one set for
+ *          every sample)
+ * Sizes: b, t, h >= 0 and 1 <= d <= 2^20, b <= 65535 and t * h * d < 2^31 (else
+ * TERN_ERR_SHAPE); a zero size is a no-op.  Axes outside their limits:
+ * TERN_ERR_ARG.  Strides >= 0 (else TERN_ERR_STRIDE).  x, y aligned to their
+ * element, pos to 4 bytes (else TERN_ERR_ALIGN).
+ */
+tern_status tern_rope(const tern_heads* x, const tern_heads* y, tern_dtype dtype, int64_t b,
+                      int64_t t, int64_t h, int64_t d, const float* pos, int64_t pos_batch,
+                      int64_t pos_token, const tern_rope_axes* axes, int inverse, void* stream);
+
+/* Norm of a row: none, layer norm (mean and variance) or RMS norm. */
+typedef enum { TERN_NORM_NONE = 0, TERN_NORM_LAYER = 1, TERN_NORM_RMS = 2 } tern_norm;
+
+#define TERN_RESIDUAL_NORM_MAX_C 8192
+
+/*
+ * One boundary between two blocks of a residual stream.  With a row's sample
+ * i = row / tokens,
+ *   z     = post(y) (.) post_weight
+ *   r_out = r + residual_scale * gate[i] (.) z            (rounded to r_dtype)
+ *   h     = (pre(r_out) (.) pre_weight) (.) (1 + scale[i]) + shift[i]
+ * post and pre are norms over the c channels of a row,
+ *   layer: (x - mean) / sqrt(mean((x - mean)^2) + eps),   rms: x / sqrt(mean(x^2) + eps),
+ * pre taken of r_out as it is stored.  A NULL weight is 1, a NULL gate 1, a
+ * NULL scale or shift 0.
+ */
+typedef struct {
+  int64_t m;      /* rows (tokens of all samples) */
+  int64_t c;      /* channels */
+  int64_t tokens; /* rows of one sample; the last sample may have fewer */
+  tern_dtype r_dtype;
+  tern_norm pre;  /* LAYER or RMS */
+  tern_norm post; /* NONE, LAYER or RMS */
+  float eps;      /* >= 0 */
+  float residual_scale;
+  const float* pre_weight;  /* [c] or NULL */
+  const float* post_weight; /* [c] or NULL; NULL when post is NONE */
+  const float* gate;        /* [samples, ldgate] or NULL */
+  int64_t ldgate;
+  const float* scale; /* [samples, ldscale] or NULL */
+  int64_t ldscale;
+  const float* shift; /* [samples, ldshift] or NULL */
+  int64_t ldshift;
+} tern_residual_norm_args;
+
+/*
+ * tern_residual_norm: the forward pass of a boundary (above), in fp32.
+ *
+ *   r      [m, ldr] residual stream of r_dtype
+ *   y      [m, ldy] bf16 output of the block before, or NULL: r_out = r is then
+ *          not written (r_out is ignored), h is taken of r
+ *   r_out  [m, ldro] of r_dtype; may be r itself (same ld)
+ *   h      [m, ldh] bf16 input of the block after, or NULL: only r_out is written
+ *   stats  NULL or [m, 4] fp32, 16-byte aligned: mean and 1 / sqrt(...) of pre,
+ *          then of post (0 where there is none), for the backward pass
+ * Sizes: m >= 0, 1 <= c <= TERN_RESIDUAL_NORM_MAX_C, tokens >= 1 and
+ * m <= 2^31 - 1 (else TERN_ERR_SHAPE); m == 0 is a no-op.  Unknown norms,
+ * pre == NONE with h, post_weight without post or eps < 0: TERN_ERR_ARG.  y and h
+ * both NULL: TERN_ERR_NULL.  Every ld >= c (else TERN_ERR_STRIDE).  Pointers
+ * aligned to their element (else TERN_ERR_ALIGN); rows that start at multiples
+ * of 8 elements are read and written in 16-byte pieces.
+ */
+tern_status tern_residual_norm(const tern_residual_norm_args* args, const void* r, int64_t ldr,
+                               const void* y_bf16, int64_t ldy, void* r_out, int64_t ldro,
+                               void* h_bf16, int64_t ldh, float* stats, void* stream);
+
+/*
+ * tern_residual_norm_bwd: the gradients of a boundary.  With n and zn the
+ * normalised rows of r_out and y (recomputed from them and stats),
+ *   g      = dh (.) (1 + scale[i]) (.) pre_weight
+ *   dr     = dr_out + rstd * (g - n mean(g n) - [layer] mean(g))
+ *   dz     = residual_scale * gate[i] (.) dr
+ *   dy     = dz through post in the same way (dz (.) post_weight, zn)
+ *   dgate[i]  = residual_scale * sum z (.) dr      dscale[i] = sum dh (.) n (.) pre_weight
+ *   dshift[i] = sum dh      dpre_weight = sum dh (.) (1 + scale) (.) n
+ *   dpost_weight = sum dz (.) zn
+ * the sums over a sample's rows (the weights' over all rows) in fp32 in an order
+ * fixed by the sizes: repeated calls give identical bits.
+ *
+ *   dr_out [m, lddro] of r_dtype, or NULL (0)
+ *   dh     [m, lddh] bf16, or NULL (h was not used; dscale, dshift and
+ *          dpre_weight must then be NULL); one of dr_out and dh is needed
+ *   r_out  [m, ldro] as stored by the forward pass (r where y was NULL); not
+ *          read without dh
+ *   y      [m, ldy] bf16 as in the forward pass, or NULL (dy, dgate and
+ *          dpost_weight must then be NULL)
+ *   stats  [m, 4] from the forward pass
+ *   dr     [m, lddr] of r_dtype; may be dr_out itself (same ld)
+ *   dy     [m, lddy] bf16, or NULL when y is NULL
+ *   dgate, dscale, dshift   [samples, c] fp32 contiguous, or NULL
+ *   dpre_weight, dpost_weight   [c] fp32, or NULL
+ *   workspace  at least tern_residual_norm_bwd_workspace(args) bytes, 16-byte
+ *          aligned (TERN_ERR_ALIGN), owned by the caller and overwritten
+ *          (workspace_bytes smaller: TERN_ERR_SHAPE)
+ * Sizes, strides and the rest as tern_residual_norm; m == 0 writes zeros into
+ * dpre_weight and dpost_weight.
+ */
+tern_status tern_residual_norm_bwd(const tern_residual_norm_args* args, const void* dr_out,
+                                   int64_t lddro, const void* dh_bf16, int64_t lddh,
+                                   const void* r_out, int64_t ldro, const void* y_bf16,
+                                   int64_t ldy, const float* stats, void* dr, int64_t lddr,
+                                   void* dy_bf16, int64_t lddy, float* dgate, float* dscale,
+                                   float* dshift, float* dpre_weight, float* dpost_weight,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tern_residual_norm_bwd needs for these sizes (0 for
+ * sizes that it refuses). */
+int64_t tern_residual_norm_bwd_workspace(const tern_residual_norm_args* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,229 @@
+"""ctypes binding of libternary's transformer-block operators: argument
+marshalling only, in the manner of ``_binding``.
+
+``rope``, ``residual_norm`` and ``residual_norm_backward`` (and the attention
+calls) check that the torch tensors they are given are on the GPU with the
+documented dtypes and a unit stride along channels, allocate the outputs, and
+call the C entry points of ``include/ternary.h``.  All arithmetic runs in the
+library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+import struct
+
+import torch
+
+from . import _binding as _b
+from ._binding import _check, _lib, _mat, _stream, _vec
+
+TERN_ROPE_INTERLEAVED = 0
+TERN_ROPE_HALVES = 1
+TERN_ROPE_MAX_AXES = 4
+TERN_ROPE_MAX_PAIRS = 128
+TERN_NORM_NONE = 0
+TERN_NORM_LAYER = 1
+TERN_NORM_RMS = 2
+TERN_RESIDUAL_NORM_MAX_C = 8192
+
+_i64, _vp, _bytes = ctypes.c_int64, ctypes.c_void_p, ctypes.c_char_p
+# The C structs travel as packed bytes of the same layout.
+_heads_struct = struct.Struct("@4q").pack
+_axes_struct = struct.Struct("@5id2i").pack  # (the layout, then padding to the double's size)
+_norm_struct = struct.Struct("@3q3i2f4x3PqPqPq").pack
+
+_lib.tern_rope.argtypes = [_bytes, _bytes, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _i64,
+                           _bytes, ctypes.c_int, _vp]
+_lib.tern_rope.restype = ctypes.c_int
+_lib.tern_residual_norm.argtypes = [_bytes] + [_vp, _i64] * 4 + [_vp, _vp]
+_lib.tern_residual_norm.restype = ctypes.c_int
+_lib.tern_residual_norm_bwd.argtypes = ([_bytes] + [_vp, _i64] * 4 + [_vp] + [_vp, _i64] * 2 +
+                                        [_vp] * 6 + [_i64, _vp])
+_lib.tern_residual_norm_bwd.restype = ctypes.c_int
+_lib.tern_residual_norm_bwd_workspace.argtypes = [_bytes]
+_lib.tern_residual_norm_bwd_workspace.restype = ctypes.c_int64
+
+_LAYOUTS = {"interleaved": TERN_ROPE_INTERLEAVED, "halves": TERN_ROPE_HALVES}
+_NORMS = {None: TERN_NORM_NONE, "layer": TERN_NORM_LAYER, "rms": TERN_NORM_RMS}
+_TYPES = {torch.float32: _b.TERN_F32, torch.bfloat16: _b.TERN_BF16}
+
+
+def _heads(a: torch.Tensor, name: str, dtypes) -> bytes:
+    """The tern_heads of a [batch, tokens, heads, width] view."""
+    if not isinstance(a, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not a.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor, got {a.device}")
+    if a.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {a.dtype}, expected one of {dtypes}")
+    if a.dim() != 4:
+        raise ValueError(f"{name} must be [batch, tokens, heads, width]")
+    b, t, h, d = a.shape
+    sb, st, sh, sd = a.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name} must have consecutive channels (unit last stride)")
+    # The stride of an axis of one element is never used.
+    return _heads_struct(a.data_ptr(), sb if b > 1 else 0, st if t > 1 else 0, sh if h > 1 else 0)
+
+
+@functools.lru_cache(maxsize=64)
+def _axes(axes, theta: float, layout: str) -> bytes:
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {tuple(_LAYOUTS)}, got {layout!r}")
+    if not 1 <= len(axes) <= TERN_ROPE_MAX_AXES:
+        raise ValueError(f"1 to {TERN_ROPE_MAX_AXES} axes, got {len(axes)}")
+    width = list(axes) + [0] * (TERN_ROPE_MAX_AXES - len(axes))
+    return _axes_struct(len(axes), *width, theta, _LAYOUTS[layout], 0)
+
+
+def rope(x: torch.Tensor, pos: torch.Tensor, axes, theta: float = 10000.0,
+         layout: str = "interleaved", inverse: bool = False, out: torch.Tensor | None = None,
+         stream=None) -> torch.Tensor:
+    """Rotary positions with several axes: ``x`` [b, t, h, d] (fp32 or bf16, any
+    strides with consecutive channels) turned by ``pos`` fp32 [b, t, n] (or
+    [t, n], the same for every sample), axis i on the next ``axes[i]`` channels.
+    ``layout`` pairs channels (2p, 2p + 1) ("interleaved") or (p, p + P)
+    ("halves").  ``inverse`` is the transpose (the gradient).  ``out`` may be
+    ``x`` itself; by default a new contiguous tensor."""
+    axes = tuple(axes)
+    xs = _heads(x, "x", _TYPES)
+    b, t, h, d = x.shape
+    if out is None:
+        out = torch.empty((b, t, h, d), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have the shape and dtype of x")
+    if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype != torch.float32:
+        raise TypeError("pos must be a GPU tensor of dtype torch.float32")
+    n = len(axes)
+    shape = tuple(pos.shape)
+    if shape not in ((t, n), (b, t, n), (1, t, n)):
+        raise ValueError(f"pos must be [t, {n}] or [b, t, {n}] for x {tuple(x.shape)}")
+    if n > 1 and pos.stride(-1) != 1:
+        raise ValueError("pos must have consecutive axes (unit last stride)")
+    pos_batch = pos.stride(0) if len(shape) == 3 and shape[0] > 1 else 0
+    pos_token = pos.stride(-2) if t > 1 else 0
+    _check("tern_rope", _lib.tern_rope(xs, _heads(out, "out", _TYPES), _TYPES[x.dtype], b, t, h, d,
+                                       pos.data_ptr(), pos_batch, pos_token,
+                                       _axes(axes, float(theta), layout), 1 if inverse else 0,
+                                       _stream(stream)))
+    return out
+
+
+def _row_vectors(a, name: str, samples: int, c: int):
+    """(pointer, pitch) of a [samples, c] fp32 matrix or None."""
+    if a is None:
+        return 0, 0
+    ld = _mat(a, name, (torch.float32,))
+    if a.shape[0] != samples or a.shape[1] != c:
+        raise ValueError(f"{name} must be [{samples}, {c}] (one row per sample)")
+    return a.data_ptr(), max(ld, c)
+
+
+def _weight(a, name: str, c: int) -> int:
+    if a is None:
+        return 0
+    _vec(a, name, torch.float32)
+    if a.shape[0] != c:
+        raise ValueError(f"{name} must be [{c}]")
+    return a.data_ptr()
+
+
+def _norm_args(m, c, dtype, tokens, pre, post, eps, residual_scale, pre_weight, post_weight, gate,
+               scale, shift):
+    if pre not in _NORMS or post not in _NORMS:
+        raise ValueError(f"pre and post must be one of {tuple(_NORMS)}")
+    tokens = max(1, m) if tokens is None else int(tokens)
+    if tokens < 1:
+        raise ValueError("tokens must be at least 1")
+    samples = -(-m // tokens)
+    return _norm_struct(m, c, tokens, _TYPES[dtype], _NORMS[pre], _NORMS[post], eps, residual_scale,
+                        _weight(pre_weight, "pre_weight", c),
+                        _weight(post_weight, "post_weight", c),
+                        *_row_vectors(gate, "gate", samples, c),
+                        *_row_vectors(scale, "scale", samples, c),
+                        *_row_vectors(shift, "shift", samples, c)), samples
+
+
+def _rows(a, name: str, dtypes, shape):
+    """(pointer, pitch) of an [m, c] matrix or None."""
+    if a is None:
+        return 0, 0
+    ld = _mat(a, name, dtypes)
+    if a.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(a.shape)}")
+    return a.data_ptr(), ld
+
+
+def residual_norm(r: torch.Tensor, y: torch.Tensor | None = None, *, gate=None, scale=None,
+                  shift=None, tokens: int | None = None, pre: str | None = "layer",
+                  post: str | None = None, pre_weight=None, post_weight=None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, with_stats: bool = False,
+                  stream=None):
+    """The boundary between two blocks: ``r_out = r + residual_scale * gate *
+    post(y) * post_weight`` and ``h = pre(r_out) * pre_weight * (1 + scale) +
+    shift``.
+
+    ``r`` [m, c] fp32 or bf16, ``y`` bf16 [m, c] or None (``r_out`` is then
+    ``r`` itself); ``gate``, ``scale``, ``shift`` fp32 [samples, c] (any pitch,
+    so chunks of one modulation matrix) for samples of ``tokens`` rows (default:
+    one sample), the weights fp32 [c]; ``pre`` and ``post`` "layer", "rms" or
+    None (``pre`` None: no ``h``).  Returns ``(r_out, h)`` with ``h`` bf16, and
+    with ``with_stats`` the fp32 [m, 4] statistics for the backward pass."""
+    ldr = _mat(r, "r", _TYPES)
+    m, c = r.shape
+    args, _ = _norm_args(m, c, r.dtype, tokens, pre, post, eps, residual_scale, pre_weight,
+                         post_weight, gate, scale, shift)
+    yp, ldy = _rows(y, "y", (torch.bfloat16,), r.shape)
+    r_out = r if y is None else torch.empty((m, c), dtype=r.dtype, device=r.device)
+    h = None if pre is None else torch.empty((m, c), dtype=torch.bfloat16, device=r.device)
+    stats = torch.empty((m, 4), dtype=torch.float32, device=r.device) if with_stats else None
+    _check("tern_residual_norm", _lib.tern_residual_norm(
+        args, r.data_ptr(), ldr, yp, ldy, r_out.data_ptr(), c, None if h is None else h.data_ptr(),
+        c, None if stats is None else stats.data_ptr(), _stream(stream)))
+    return (r_out, h, stats) if with_stats else (r_out, h)
+
+
+def residual_norm_backward(dr_out, dh, r_out: torch.Tensor, y, stats: torch.Tensor, *, gate=None,
+                           scale=None, with_shift: bool = True, tokens: int | None = None,
+                           pre: str | None = "layer", post: str | None = None, pre_weight=None,
+                           post_weight=None, residual_scale: float = 1.0, eps: float = 1e-6,
+                           stream=None):
+    """Gradients of ``residual_norm``: ``(dr, dy, dgate, dscale, dshift,
+    dpre_weight, dpost_weight)`` from ``dr_out`` (``r``'s dtype, or None) and
+    ``dh`` (bf16, or None), the stored ``r_out`` (``r`` where ``y`` was None), ``y`` and ``stats``.
+    None stands for the gradient of what is not there (``dshift`` without
+    ``with_shift``)."""
+    ldro = _mat(r_out, "r_out", _TYPES)
+    m, c = r_out.shape
+    shape, dtype, device = r_out.shape, r_out.dtype, r_out.device
+    args, samples = _norm_args(m, c, dtype, tokens, pre, post, eps, residual_scale, pre_weight,
+                               post_weight, gate, scale, None)
+    drop, lddro = _rows(dr_out, "dr_out", (dtype,), shape)
+    dhp, lddh = _rows(dh, "dh", (torch.bfloat16,), shape)
+    yp, ldy = _rows(y, "y", (torch.bfloat16,), shape)
+    if _mat(stats, "stats", (torch.float32,)) != 4 and m > 1 or tuple(stats.shape) != (m, 4):
+        raise ValueError(f"stats must be a contiguous [{m}, 4] tensor")
+    dr = torch.empty((m, c), dtype=dtype, device=device)
+    dy = None if y is None else torch.empty((m, c), dtype=torch.bfloat16, device=device)
+
+    def sums(wanted, *size):
+        return torch.empty(size, dtype=torch.float32, device=device) if wanted else None
+
+    dgate = sums(gate is not None and y is not None, samples, c)
+    dscale = sums(scale is not None and dh is not None, samples, c)
+    dshift = sums(with_shift and dh is not None, samples, c)
+    dpre = sums(pre_weight is not None and dh is not None, c)
+    dpost = sums(post_weight is not None and y is not None, c)
+    need = _lib.tern_residual_norm_bwd_workspace(args)
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+
+    def ptr(a):
+        return None if a is None else a.data_ptr()
+
+    _check("tern_residual_norm_bwd", _lib.tern_residual_norm_bwd(
+        args, drop, lddro, dhp, lddh, r_out.data_ptr(), ldro, yp, ldy, stats.data_ptr(),
+        dr.data_ptr(), c, ptr(dy), c, ptr(dgate), ptr(dscale), ptr(dshift), ptr(dpre), ptr(dpost),
+        workspace.data_ptr(), need, _stream(stream)))
+    return dr, dy, dgate, dscale, dshift, dpre, dpost

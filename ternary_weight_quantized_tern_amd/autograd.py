@@ -1,4 +1,7 @@
-"""The ternary linear layer as a torch autograd function, for training the
+"""The ternary linear layer, and the operators of the block around it, as torch
+autograd functions.
+
+ternary_linear: for training the
 latent full-precision weights in the loop (quantization-aware training as in
 "TerDiT: Ternary Diffusion Models with Transformers", abstract).
 
@@ -15,6 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import _binding as _b
+from . import _block as _k
 
 
 class TernaryLinearFunction(torch.autograd.Function):
@@ -53,3 +57,72 @@ def ternary_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     """The ternary linear layer with straight-through gradients (see
     TernaryLinearFunction)."""
     return TernaryLinearFunction.apply(x, w)
+
+
+class RotaryFunction(torch.autograd.Function):
+    """Rotary positions (tern_rope); the gradient is the same call with the
+    angles negated.  Positions have no gradient."""
+
+    @staticmethod
+    def forward(ctx, x, pos, axes, theta, layout):
+        ctx.save_for_backward(pos)
+        ctx.plan = (axes, theta, layout)
+        return _k.rope(x.detach(), pos, axes, theta, layout)
+
+    @staticmethod
+    def backward(ctx, dy):
+        (pos,) = ctx.saved_tensors
+        axes, theta, layout = ctx.plan
+        if dy.stride(-1) != 1:
+            dy = dy.contiguous()
+        return _k.rope(dy, pos, axes, theta, layout, inverse=True), None, None, None, None
+
+
+def rotary(x: torch.Tensor, pos: torch.Tensor, axes, theta: float = 10000.0,
+           layout: str = "interleaved") -> torch.Tensor:
+    """``rope`` with a gradient."""
+    return RotaryFunction.apply(x, pos, tuple(axes), theta, layout)
+
+
+def _rows_of(t):
+    """A gradient as a row-major matrix."""
+    return t if t is None or t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+
+
+class BlockBoundaryFunction(torch.autograd.Function):
+    """residual_norm with gradients of the stream, the branch, the modulation
+    vectors and the weights (tern_residual_norm_bwd)."""
+
+    @staticmethod
+    def forward(ctx, r, y, gate, scale, shift, pre_weight, post_weight, options):
+        r_out, h, stats = _k.residual_norm(r.detach(), y, gate=gate, scale=scale, shift=shift,
+                                           pre_weight=pre_weight, post_weight=post_weight,
+                                           with_stats=True, **options)
+        ctx.save_for_backward(r_out, y, stats, gate, scale, pre_weight, post_weight)
+        ctx.options, ctx.with_shift = options, shift is not None
+        ctx.set_materialize_grads(False)
+        if y is None:
+            ctx.mark_non_differentiable(r_out)
+        return r_out, h
+
+    @staticmethod
+    def backward(ctx, dr_out, dh):
+        r_out, y, stats, gate, scale, pre_weight, post_weight = ctx.saved_tensors
+        if dr_out is None and dh is None:
+            return (None,) * 8
+        dr, dy, dgate, dscale, dshift, dpre, dpost = _k.residual_norm_backward(
+            _rows_of(dr_out), _rows_of(dh), r_out, y, stats, gate=gate, scale=scale,
+            with_shift=ctx.with_shift, pre_weight=pre_weight, post_weight=post_weight,
+            **ctx.options)
+        return dr, dy, dgate, dscale, dshift, dpre, dpost, None
+
+
+def block_boundary(r, y=None, *, gate=None, scale=None, shift=None, tokens=None, pre="layer",
+                   post=None, pre_weight=None, post_weight=None, residual_scale=1.0, eps=1e-6):
+    """``residual_norm`` with gradients: ``(r_out, h)``, or with ``y`` None ``h``
+    alone and with ``pre`` None ``r_out`` alone."""
+    options = {"tokens": tokens, "pre": pre, "post": post, "residual_scale": residual_scale,
+               "eps": eps}
+    r_out, h = BlockBoundaryFunction.apply(r, y, gate, scale, shift, pre_weight, post_weight,
+                                           options)
+    return h if y is None else r_out if pre is None else (r_out, h)

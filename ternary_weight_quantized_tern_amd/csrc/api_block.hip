@@ -1,0 +1,228 @@
+// C-ABI of the transformer-block operators (declared in include/ternary.h):
+// host-side argument validation, then asynchronous launches on the caller's
+// stream.  No HIP call is made before every argument has been checked, and
+// the library keeps no state between calls.
+#include <math.h>
+
+#include "ternary.h"
+
+#include "internal.h"
+
+namespace {
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+inline tern_status from_hip(hipError_t e) { return e == hipSuccess ? TERN_OK : TERN_ERR_HIP; }
+
+constexpr int64_t kMaxInt = 2147483647;  // 2^31 - 1
+
+inline bool strides_ok(const tern_heads* v) { return v->batch >= 0 && v->token >= 0 && v->head >= 0; }
+
+tern_status check_norm(const tern_residual_norm_args* a) {
+  if (a == nullptr) return TERN_ERR_NULL;
+  if (a->r_dtype != TERN_F32 && a->r_dtype != TERN_BF16) return TERN_ERR_DTYPE;
+  if ((a->pre != TERN_NORM_NONE && a->pre != TERN_NORM_LAYER && a->pre != TERN_NORM_RMS) ||
+      (a->post != TERN_NORM_NONE && a->post != TERN_NORM_LAYER && a->post != TERN_NORM_RMS) ||
+      !(a->eps >= 0.0f) || !isfinite(a->eps) || !isfinite(a->residual_scale) ||
+      (a->post == TERN_NORM_NONE && a->post_weight != nullptr))
+    return TERN_ERR_ARG;
+  if (a->m < 0 || a->m > kMaxInt || a->c < 1 || a->c > TERN_RESIDUAL_NORM_MAX_C || a->tokens < 1)
+    return TERN_ERR_SHAPE;
+  return TERN_OK;
+}
+
+// A sample's vectors: their pitches and alignment.
+tern_status check_vectors(const tern_residual_norm_args* a, bool with_shift) {
+  if ((a->gate && a->ldgate < a->c) || (a->scale && a->ldscale < a->c) ||
+      (with_shift && a->shift && a->ldshift < a->c))
+    return TERN_ERR_STRIDE;
+  if (!aligned(a->pre_weight, 4) || !aligned(a->post_weight, 4) || !aligned(a->gate, 4) ||
+      !aligned(a->scale, 4) || (with_shift && !aligned(a->shift, 4)))
+    return TERN_ERR_ALIGN;
+  return TERN_OK;
+}
+
+inline uintptr_t size_of(tern_dtype t) { return t == TERN_F32 ? 4 : 2; }
+
+}  // namespace
+
+extern "C" {
+
+tern_status tern_rope(const tern_heads* x, const tern_heads* y, tern_dtype dtype, int64_t b,
+                      int64_t t, int64_t h, int64_t d, const float* pos, int64_t pos_batch,
+                      int64_t pos_token, const tern_rope_axes* axes, int inverse, void* stream) {
+  if (dtype != TERN_F32 && dtype != TERN_BF16) return TERN_ERR_DTYPE;
+  if (axes == nullptr) return TERN_ERR_NULL;
+  if (axes->count < 1 || axes->count > TERN_ROPE_MAX_AXES || !(axes->theta > 0.0) ||
+      !isfinite(axes->theta) ||
+      (axes->layout != TERN_ROPE_INTERLEAVED && axes->layout != TERN_ROPE_HALVES))
+    return TERN_ERR_ARG;
+  int64_t turned = 0;
+  for (int a = 0; a < axes->count; ++a) {
+    if (axes->width[a] < 0 || axes->width[a] % 2 != 0) return TERN_ERR_ARG;
+    turned += axes->width[a];
+  }
+  if (turned > 2 * TERN_ROPE_MAX_PAIRS) return TERN_ERR_ARG;
+  if (b < 0 || b > 65535 || t < 0 || t > kMaxInt || h < 0 || h > kMaxInt || d < 1 ||
+      d > (int64_t(1) << 20))
+    return TERN_ERR_SHAPE;
+  if (turned > d) return TERN_ERR_ARG;
+  if (b == 0 || t == 0 || h == 0) return TERN_OK;
+  if (t > kMaxInt / h || t * h > kMaxInt / d) return TERN_ERR_SHAPE;
+  if (x == nullptr || y == nullptr || x->data == nullptr || y->data == nullptr || pos == nullptr)
+    return TERN_ERR_NULL;
+  if (!strides_ok(x) || !strides_ok(y) || pos_batch < 0 || pos_token < 0) return TERN_ERR_STRIDE;
+  if (!aligned(x->data, size_of(dtype)) || !aligned(y->data, size_of(dtype)) || !aligned(pos, 4))
+    return TERN_ERR_ALIGN;
+  tern::RopeParams p = {};
+  p.x = *x;
+  p.y = *y;
+  p.pos = pos;
+  p.pos_batch = pos_batch;
+  p.pos_token = pos_token;
+  p.h = static_cast<int32_t>(h);
+  p.d = static_cast<int32_t>(d);
+  p.pairs = static_cast<int32_t>(turned / 2);
+  p.inverse = inverse != 0;
+  for (int32_t& f : p.first) f = p.pairs;
+  int pair = 0;
+  for (int a = 0; a < axes->count; ++a) {
+    if (a > 0) p.first[a - 1] = pair;
+    const int w = axes->width[a];
+    const double step = w > 0 ? pow(axes->theta, -2.0 / w) : 1.0;
+    double turn = 0.5 / M_PI;
+    for (int i = 0; i < w / 2; ++i, ++pair, turn *= step) {
+      p.turn[pair] = static_cast<float>(turn);
+      p.turn_tail[pair] = static_cast<float>(turn - static_cast<double>(p.turn[pair]));
+    }
+  }
+  return from_hip(tern::launch_rope(p, dtype == TERN_BF16, axes->layout == TERN_ROPE_HALVES, b, t,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+tern_status tern_residual_norm(const tern_residual_norm_args* args, const void* r, int64_t ldr,
+                               const void* y_bf16, int64_t ldy, void* r_out, int64_t ldro,
+                               void* h_bf16, int64_t ldh, float* stats, void* stream) {
+  const tern_status bad = check_norm(args);
+  if (bad != TERN_OK) return bad;
+  const tern_residual_norm_args& a = *args;
+  if (h_bf16 != nullptr && a.pre == TERN_NORM_NONE) return TERN_ERR_ARG;
+  if (a.m == 0) return TERN_OK;
+  if (r == nullptr || (y_bf16 == nullptr && h_bf16 == nullptr) ||
+      (y_bf16 != nullptr && r_out == nullptr))
+    return TERN_ERR_NULL;
+  if (ldr < a.c || (y_bf16 && (ldy < a.c || ldro < a.c)) || (h_bf16 && ldh < a.c))
+    return TERN_ERR_STRIDE;
+  const tern_status vectors = check_vectors(args, true);
+  if (vectors != TERN_OK) return vectors;
+  const uintptr_t esz = size_of(a.r_dtype);
+  if (!aligned(r, esz) || (y_bf16 && !aligned(r_out, esz)) || !aligned(y_bf16, 2) ||
+      !aligned(h_bf16, 2) || !aligned(stats, 16))
+    return TERN_ERR_ALIGN;
+  tern::ResidualNormParams p = {};
+  p.m = a.m;
+  p.tokens = a.tokens;
+  p.c = static_cast<int32_t>(a.c);
+  p.pre = a.pre;
+  p.post = a.post;
+  p.eps = a.eps;
+  p.residual_scale = a.residual_scale;
+  p.pre_weight = a.pre_weight;
+  p.post_weight = a.post_weight;
+  p.gate = a.gate;
+  p.ldgate = a.gate ? a.ldgate : 0;
+  p.scale = a.scale;
+  p.ldscale = a.scale ? a.ldscale : 0;
+  p.shift = a.shift;
+  p.ldshift = a.shift ? a.ldshift : 0;
+  p.r = r;
+  p.ldr = ldr;
+  p.y = y_bf16;
+  p.ldy = y_bf16 ? ldy : 0;
+  p.r_out = y_bf16 ? r_out : nullptr;
+  p.ldro = y_bf16 ? ldro : 0;
+  p.h = h_bf16;
+  p.ldh = h_bf16 ? ldh : 0;
+  p.stats = stats;
+  return from_hip(tern::launch_residual_norm(p, a.r_dtype == TERN_BF16,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int64_t tern_residual_norm_bwd_workspace(const tern_residual_norm_args* args) {
+  if (check_norm(args) != TERN_OK) return 0;
+  return tern::residual_norm_bwd_workspace(args->m, args->c, args->tokens);
+}
+
+tern_status tern_residual_norm_bwd(const tern_residual_norm_args* args, const void* dr_out,
+                                   int64_t lddro, const void* dh_bf16, int64_t lddh,
+                                   const void* r_out, int64_t ldro, const void* y_bf16,
+                                   int64_t ldy, const float* stats, void* dr, int64_t lddr,
+                                   void* dy_bf16, int64_t lddy, float* dgate, float* dscale,
+                                   float* dshift, float* dpre_weight, float* dpost_weight,
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+  const tern_status bad = check_norm(args);
+  if (bad != TERN_OK) return bad;
+  const tern_residual_norm_args& a = *args;
+  if (dh_bf16 != nullptr && a.pre == TERN_NORM_NONE) return TERN_ERR_ARG;
+  // Gradients of what the forward pass did not have.
+  if (a.post == TERN_NORM_NONE && dpost_weight) return TERN_ERR_ARG;
+  if (a.m > 0 && ((dh_bf16 == nullptr && (dscale || dshift || dpre_weight)) ||
+                  (y_bf16 == nullptr && (dy_bf16 || dgate || dpost_weight))))
+    return TERN_ERR_ARG;
+  if (a.m > 0) {
+    if (workspace_bytes < tern::residual_norm_bwd_workspace(a.m, a.c, a.tokens))
+      return TERN_ERR_SHAPE;
+    if ((dr_out == nullptr && dh_bf16 == nullptr) || (dh_bf16 && r_out == nullptr) ||
+        stats == nullptr || dr == nullptr || (y_bf16 && dy_bf16 == nullptr) ||
+        workspace == nullptr)
+      return TERN_ERR_NULL;
+    if ((dr_out && lddro < a.c) || (dh_bf16 && (lddh < a.c || ldro < a.c)) || lddr < a.c ||
+        (y_bf16 && (ldy < a.c || lddy < a.c)))
+      return TERN_ERR_STRIDE;
+    const tern_status vectors = check_vectors(args, false);
+    if (vectors != TERN_OK) return vectors;
+    const uintptr_t esz = size_of(a.r_dtype);
+    if (!aligned(dr_out, esz) || (dh_bf16 && !aligned(r_out, esz)) || !aligned(dr, esz) ||
+        !aligned(dh_bf16, 2) || !aligned(y_bf16, 2) || !aligned(dy_bf16, 2) ||
+        !aligned(stats, 16) || !aligned(workspace, 16))
+      return TERN_ERR_ALIGN;
+  }
+  if (!aligned(dgate, 4) || !aligned(dscale, 4) || !aligned(dshift, 4) ||
+      !aligned(dpre_weight, 4) || !aligned(dpost_weight, 4))
+    return TERN_ERR_ALIGN;
+  tern::ResidualNormBwdParams p = {};
+  p.m = a.m;
+  p.tokens = a.tokens;
+  p.c = static_cast<int32_t>(a.c);
+  p.pre = a.pre;
+  p.post = a.post;
+  p.residual_scale = a.residual_scale;
+  p.pre_weight = a.pre_weight;
+  p.post_weight = a.post_weight;
+  p.gate = a.gate;
+  p.ldgate = a.gate ? a.ldgate : 0;
+  p.scale = a.scale;
+  p.ldscale = a.scale ? a.ldscale : 0;
+  p.dr_out = dr_out;
+  p.lddro = dr_out ? lddro : 0;
+  p.dh = dh_bf16;
+  p.lddh = dh_bf16 ? lddh : 0;
+  p.r_out = dh_bf16 ? r_out : nullptr;
+  p.ldro = dh_bf16 ? ldro : 0;
+  p.y = y_bf16;
+  p.ldy = y_bf16 ? ldy : 0;
+  p.stats = stats;
+  p.dr = dr;
+  p.lddr = lddr;
+  p.dy = dy_bf16;
+  p.lddy = y_bf16 ? lddy : 0;
+  p.dgate = dgate;
+  p.dscale = dscale;
+  p.dshift = dshift;
+  p.dpre_weight = dpre_weight;
+  p.dpost_weight = dpost_weight;
+  return from_hip(tern::launch_residual_norm_bwd(p, a.r_dtype == TERN_BF16, workspace,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

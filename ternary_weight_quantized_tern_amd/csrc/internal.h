@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ternary.h"
+
 namespace tern {
 
 // Launch geometry and the ld / alignment facts the launchers rely on are
@@ -86,5 +88,64 @@ hipError_t launch_gemm_a8(const int8_t* q, int64_t m, int64_t k, int64_t ldq, co
                           const uint8_t* p8, int64_t n, int64_t ldp8, const float* s,
                           const float* bias, int64_t act_from, uint16_t* y, int64_t ldy,
                           hipStream_t stream);
+
+// Rotary positions.  The caller fills the first part; launch_rope the second.
+struct RopeParams {
+  tern_heads x, y;
+  const float* pos;
+  int64_t pos_batch, pos_token;
+  int32_t h, d, pairs;
+  int32_t first[TERN_ROPE_MAX_AXES - 1];  // first pair of axes 1, 2, 3 (pairs where there is none)
+  int32_t inverse;
+  float turn[TERN_ROPE_MAX_PAIRS];       // frequency in turns a position, and
+  float turn_tail[TERN_ROPE_MAX_PAIRS];  // what rounding it to fp32 left over
+
+  uint32_t items, turn_units, rest_units, lanes;
+};
+hipError_t launch_rope(RopeParams& params, bool is_bf16, bool halves, int64_t b, int64_t t,
+                       hipStream_t stream);
+
+// The boundary of two blocks of a residual stream; NULL pointers as in
+// tern_residual_norm (r_out is not used without y).  The launchers fill in what
+// follows the blank line.
+struct ResidualNormParams {
+  int64_t m, tokens;
+  int32_t c;
+  tern_norm pre, post;
+  float eps, residual_scale;
+  const float *pre_weight, *post_weight, *gate, *scale, *shift;
+  int64_t ldgate, ldscale, ldshift;
+  const void *r, *y;
+  int64_t ldr, ldy;
+  void *r_out, *h;
+  int64_t ldro, ldh;
+  float* stats;
+
+  int64_t rows;     // rows a workgroup walks over
+  int32_t threads;  // threads to a row
+};
+hipError_t launch_residual_norm(ResidualNormParams& params, bool r_is_bf16, hipStream_t stream);
+
+struct ResidualNormBwdParams {
+  int64_t m, tokens;
+  int32_t c;
+  tern_norm pre, post;
+  float residual_scale;
+  const float *pre_weight, *post_weight, *gate, *scale;
+  int64_t ldgate, ldscale;
+  const void *dr_out, *dh, *r_out, *y;
+  int64_t lddro, lddh, ldro, ldy;
+  const float* stats;
+  void *dr, *dy;
+  int64_t lddr, lddy;
+  float *dgate, *dscale, *dshift, *dpre_weight, *dpost_weight;
+
+  int64_t rows, samples;   // rows a workgroup walks over
+  int32_t threads, slots;  // threads to a row, rows side by side
+  float *part, *totals;    // in the workspace
+};
+int64_t residual_norm_bwd_workspace(int64_t m, int64_t c, int64_t tokens);
+hipError_t launch_residual_norm_bwd(ResidualNormBwdParams& params, bool r_is_bf16, void* workspace,
+                                    hipStream_t stream);
 
 }  // namespace tern

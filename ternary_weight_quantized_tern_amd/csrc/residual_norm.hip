@@ -1,0 +1,660 @@
+// The boundary between two blocks of a residual stream, forward and backward:
+//   z = post(y) w_post,  r' = r + alpha gate z,  h = pre(r') w_pre (1 + scale) + shift
+// with post and pre layer or RMS norms of a row, and gate, scale and shift one
+// vector for each sample.
+//
+// Bound by memory: forward r, y -> r', h (8 bytes a channel in bf16), backward
+// dr', dh, r', y -> dr, dy (12 bytes).  So a row is read once, kept in
+// registers through both norms, and written once.
+//
+// A workgroup walks over consecutive rows, W waves to a row with eight (or 16)
+// channels a lane, so that the sample's vectors, and in the backward pass the
+// three sums over rows, stay in registers from row to row.  W is the row's
+// width in waves (3 for 1152 channels, 6 for 3072): the lanes are used up and
+// few registers are needed, so many rows are in flight on a CU.  The row's sums
+// go over a wave by cross-lane moves and over waves through LDS, one barrier a
+// sum; the next row's loads are issued before them.
+//
+// Statistics are in fp32 and centred: a wave takes its own mean and the
+// squares about it, and the waves' are joined by the shift formula
+// sum (x - m)^2 = sum_w (Q_w + n_w (m_w - m)^2), so that a stream with a large
+// mean loses nothing.
+//
+// Backward, the sums over rows are S = sum dh n, Z = sum dr zn and H = sum dh:
+// dscale = w_pre S, dgate = alpha w_post Z, dshift = H, and the weights'
+// gradients are sums of (1 + scale) S and alpha gate Z over samples.  A
+// workgroup writes one partial triple for each sample that it meets, a second kernel
+// adds a sample's partials in order, a third (only for weights) the samples'.
+// No atomics: the order is fixed by the sizes.
+#include "internal.h"
+#include "wave.h"
+
+namespace tern {
+namespace {
+
+using bf16 = __bf16;
+template <typename T, int N>
+using vec_t = __attribute__((ext_vector_type(N))) T;
+
+constexpr int kMaxWaves = 16;
+
+// Eight channels of a row in the type they are stored in.  WIDE: channels
+// 8 (j threads + lane) + e, 16-byte pieces.  Otherwise channels (8 j + e)
+// threads + lane, one at a time: neighbouring lanes still read neighbouring
+// channels, and any width, pitch and alignment works.
+template <typename T, bool WIDE>
+struct Piece;
+
+template <typename T>
+struct Piece<T, true> {
+  vec_t<T, 4> a, b;
+  __device__ void load(const T* row, int j, int n, int lane, int c) {
+    const int col = 8 * (j * n + lane);
+    if (col < c) {
+      a = *reinterpret_cast<const vec_t<T, 4>*>(row + col);
+      b = *reinterpret_cast<const vec_t<T, 4>*>(row + col + 4);
+    } else {
+      a = vec_t<T, 4>{};
+      b = vec_t<T, 4>{};
+    }
+  }
+  __device__ float operator[](int e) const {
+    return e < 4 ? static_cast<float>(a[e & 3]) : static_cast<float>(b[e & 3]);
+  }
+};
+
+template <>
+struct Piece<bf16, true> {
+  vec_t<bf16, 8> a;
+  __device__ void load(const bf16* row, int j, int n, int lane, int c) {
+    const int col = 8 * (j * n + lane);
+    a = vec_t<bf16, 8>{};
+    if (col < c) a = *reinterpret_cast<const vec_t<bf16, 8>*>(row + col);
+  }
+  __device__ float operator[](int e) const { return static_cast<float>(a[e]); }
+};
+
+template <typename T>
+struct Piece<T, false> {
+  T a[8];
+  __device__ void load(const T* row, int j, int n, int lane, int c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = (8 * j + e) * n + lane;
+      a[e] = col < c ? row[col] : static_cast<T>(0.0f);
+    }
+  }
+  __device__ float operator[](int e) const { return static_cast<float>(a[e]); }
+};
+
+template <bool WIDE, typename T>
+__device__ inline void store_piece(T* row, const float (&v)[8], int j, int n, int lane, int c) {
+  if constexpr (WIDE) {
+    const int col = 8 * (j * n + lane);
+    if (col >= c) return;
+    if constexpr (sizeof(T) == 2) {
+      vec_t<T, 8> o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = static_cast<T>(v[e]);
+      *reinterpret_cast<vec_t<T, 8>*>(row + col) = o;
+    } else {
+      vec_t<T, 4> o, p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[e] = v[e];
+        p[e] = v[e + 4];
+      }
+      *reinterpret_cast<vec_t<T, 4>*>(row + col) = o;
+      *reinterpret_cast<vec_t<T, 4>*>(row + col + 4) = p;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = (8 * j + e) * n + lane;
+      if (col < c) row[col] = static_cast<T>(v[e]);
+    }
+  }
+}
+
+// Eight channels of a per-channel vector, `none` where there is no vector and
+// past its end.
+template <bool WIDE>
+__device__ inline void load_vector(const float* p, float (&v)[8], float none, int j, int n,
+                                   int lane, int c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = none;
+  if (p == nullptr) return;
+  Piece<float, WIDE> x;
+  x.load(p, j, n, lane, c);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = x[e];
+}
+
+template <bool WIDE>
+__device__ inline bool inside(int j, int e, int n, int lane, int c) {
+  return (WIDE ? 8 * (j * n + lane) : (8 * j + e) * n + lane) < c;
+}
+
+// Sums over a row's waves: each wave leaves its own in LDS, two buffers in turn
+// so that one barrier a sum is enough (a wave can be at most one sum ahead of
+// the slowest reader).  `waves` waves from `first` on share a row.
+struct RowSums {
+  float4 (*buf)[kMaxWaves];
+  int first, waves, wave, turn;
+  __device__ const float4* meet(float4 mine) {
+    float4* b = buf[turn & 1];
+    ++turn;
+    if ((threadIdx.x & 63) == 0) b[wave] = mine;
+    __syncthreads();
+    return b + first;
+  }
+};
+
+// mean and 1 / sqrt(variance or mean square + eps) of a row of c values, held
+// eight by eight; values past the end are 0.
+template <int NCH, bool WIDE>
+__device__ inline void statistics(const float (&x)[NCH][8], bool layer, float eps, int n, int lane,
+                                  int c, RowSums& sums, float& mean, float& rstd) {
+  float s = 0.0f, own = 0.0f;
+  if (layer) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s += x[j][e];
+        own += inside<WIDE>(j, e, n, lane, c) ? 1.0f : 0.0f;
+      }
+    s = wave_sum(s);
+    own = wave_sum(own);
+  }
+  const float centre = layer && own > 0.0f ? s / own : 0.0f;
+  float q = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = inside<WIDE>(j, e, n, lane, c) ? x[j][e] - centre : 0.0f;
+      q = __builtin_fmaf(d, d, q);
+    }
+  q = wave_sum(q);
+  const float inv = 1.0f / static_cast<float>(c);
+  if (sums.waves > 1) {
+    const float4* b = sums.meet(make_float4(s, own, centre, q));
+    float total = 0.0f;
+    for (int w = 0; w < sums.waves; ++w) total += b[w].x;
+    mean = total * inv;
+    q = 0.0f;
+    for (int w = 0; w < sums.waves; ++w) {
+      const float d = b[w].z - mean;
+      q += b[w].w + b[w].y * d * d;  // y is 0 without a mean
+    }
+  } else {
+    mean = s * inv;
+  }
+  const float v = __builtin_fmaf(q, inv, eps);
+  // One Newton step after the hardware's reciprocal square root.
+  const float r0 = __builtin_amdgcn_rsqf(v);
+  rstd = r0 * __builtin_fmaf(-0.5f * v * r0, r0, 1.5f);
+  if (!(v > 0.0f) || rstd != rstd) rstd = r0;
+}
+
+template <typename RT, int NCH, bool WIDE>
+__global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p) {
+  __shared__ float4 meet[2][kMaxWaves];
+  const int n = p.threads, lane = threadIdx.x, c = p.c;
+  RowSums sums{meet, 0, n >> 6, lane >> 6, 0};
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows;
+  const int64_t row1 = row0 + p.rows < p.m ? row0 + p.rows : p.m;
+  const bool has_y = p.y != nullptr, has_h = p.h != nullptr;
+
+  float gate[NCH][8], scale[NCH][8], shift[NCH][8], wpre[NCH][8], wpost[NCH][8];
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    load_vector<WIDE>(p.pre_weight, wpre[j], 1.0f, j, n, lane, c);
+    load_vector<WIDE>(p.post_weight, wpost[j], 1.0f, j, n, lane, c);
+  }
+  int64_t sample = -1, sample_end = 0;
+
+  Piece<RT, WIDE> r[NCH];
+  Piece<bf16, WIDE> y[NCH];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      r[j].load(static_cast<const RT*>(p.r) + row * p.ldr, j, n, lane, c);
+      if (has_y) y[j].load(static_cast<const bf16*>(p.y) + row * p.ldy, j, n, lane, c);
+    }
+  };
+  fetch(row0);
+  for (int64_t row = row0; row < row1; ++row) {
+    if (row >= sample_end) {
+      sample = row / p.tokens;
+      sample_end = (sample + 1) * p.tokens;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        load_vector<WIDE>(p.gate ? p.gate + sample * p.ldgate : nullptr, gate[j], 1.0f, j, n, lane, c);
+        load_vector<WIDE>(p.scale ? p.scale + sample * p.ldscale : nullptr, scale[j], 0.0f, j, n, lane, c);
+        load_vector<WIDE>(p.shift ? p.shift + sample * p.ldshift : nullptr, shift[j], 0.0f, j, n, lane, c);
+      }
+    }
+    float x[NCH][8], z[NCH][8];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[j][e] = r[j][e];
+        if (has_y) z[j][e] = y[j][e];
+      }
+    if (row + 1 < row1) fetch(row + 1);
+    float mean = 0.0f, rstd = 0.0f, mean2 = 0.0f, rstd2 = 0.0f;
+    if (has_y) {
+      if (p.post != TERN_NORM_NONE) {
+        statistics<NCH, WIDE>(z, p.post == TERN_NORM_LAYER, p.eps, n, lane, c, sums, mean2, rstd2);
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[j][e] = (z[j][e] - mean2) * rstd2 * wpost[j][e];
+      }
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[j][e] = __builtin_fmaf(p.residual_scale * gate[j][e], z[j][e], x[j][e]);
+          // The norm is taken of the stream as it is stored.
+          x[j][e] = static_cast<float>(static_cast<RT>(x[j][e]));
+          if (!inside<WIDE>(j, e, n, lane, c)) x[j][e] = 0.0f;
+        }
+        store_piece<WIDE>(static_cast<RT*>(p.r_out) + row * p.ldro, x[j], j, n, lane, c);
+      }
+    }
+    if (has_h) {
+      statistics<NCH, WIDE>(x, p.pre == TERN_NORM_LAYER, p.eps, n, lane, c, sums, mean, rstd);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[j][e] = __builtin_fmaf((x[j][e] - mean) * rstd * wpre[j][e], 1.0f + scale[j][e],
+                                   shift[j][e]);
+        store_piece<WIDE>(static_cast<bf16*>(p.h) + row * p.ldh, x[j], j, n, lane, c);
+      }
+    }
+    if (p.stats != nullptr && lane == 0)
+      *reinterpret_cast<float4*>(p.stats + 4 * row) = make_float4(mean, rstd, mean2, rstd2);
+  }
+}
+
+// The gradient of a norm's input from that of its normalised row:
+//   (g - n mean(g n) - [layer] mean(g)) rstd.
+template <int NCH>
+__device__ inline void through_norm(float (&g)[NCH][8], const float (&x)[NCH][8], bool layer,
+                                    float rstd, int c, RowSums& sums) {
+  float a = 0.0f, b = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a = __builtin_fmaf(g[j][e], x[j][e], a);
+      b += g[j][e];
+    }
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if (sums.waves > 1) {
+    const float4* w = sums.meet(make_float4(a, b, 0.0f, 0.0f));
+    a = b = 0.0f;
+    for (int i = 0; i < sums.waves; ++i) {
+      a += w[i].x;
+      b += w[i].y;
+    }
+  }
+  const float inv = 1.0f / static_cast<float>(c);
+  a *= inv;
+  b = layer ? b * inv : 0.0f;
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[j][e] = (g[j][e] - b - x[j][e] * a) * rstd;
+}
+
+// p.slots rows at a time (p.threads threads each) of p.rows consecutive rows,
+// sample by sample; p.part[(workgroup + sample) * 3 + i] gets the sums of the
+// workgroup's rows of that sample (workgroup + sample is different for every
+// such pair).
+template <typename RT, int NCH, bool WIDE>
+__global__ __launch_bounds__(NCH == 1 ? 768 : 512) void residual_norm_bwd_kernel(
+    ResidualNormBwdParams p) {
+  __shared__ float4 meet[2][kMaxWaves];
+  extern __shared__ float joined[];  // [3][8 NCH threads] with more than one slot
+  const int n = p.threads, c = p.c;
+  const int slot = threadIdx.x / n, lane = threadIdx.x - slot * n;
+  RowSums sums{meet, slot * (n >> 6), n >> 6, static_cast<int>(threadIdx.x >> 6), 0};
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows;
+  const int64_t row1 = row0 + p.rows < p.m ? row0 + p.rows : p.m;
+  const bool has_y = p.y != nullptr, has_h = p.dh != nullptr, has_dr = p.dr_out != nullptr;
+
+  Piece<RT, WIDE> in_dr[NCH], in_r[NCH];
+  Piece<bf16, WIDE> in_dh[NCH], in_y[NCH];
+  float4 in_stats;
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      if (has_dr) in_dr[j].load(static_cast<const RT*>(p.dr_out) + row * p.lddro, j, n, lane, c);
+      if (has_h) {
+        in_dh[j].load(static_cast<const bf16*>(p.dh) + row * p.lddh, j, n, lane, c);
+        in_r[j].load(static_cast<const RT*>(p.r_out) + row * p.ldro, j, n, lane, c);
+      }
+      if (has_y) in_y[j].load(static_cast<const bf16*>(p.y) + row * p.ldy, j, n, lane, c);
+    }
+    in_stats = *reinterpret_cast<const float4*>(p.stats + 4 * row);
+  };
+
+  for (int64_t start = row0; start < row1;) {
+    const int64_t sample = start / p.tokens;
+    const int64_t end = (sample + 1) * p.tokens < row1 ? (sample + 1) * p.tokens : row1;
+    float gate[NCH][8], scale[NCH][8], wpre[NCH][8], wpost[NCH][8];
+    float sum_n[NCH][8], sum_z[NCH][8], sum_h[NCH][8];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      load_vector<WIDE>(p.pre_weight, wpre[j], 1.0f, j, n, lane, c);
+      load_vector<WIDE>(p.post_weight, wpost[j], 1.0f, j, n, lane, c);
+      load_vector<WIDE>(p.gate ? p.gate + sample * p.ldgate : nullptr, gate[j], 1.0f, j, n, lane, c);
+      load_vector<WIDE>(p.scale ? p.scale + sample * p.ldscale : nullptr, scale[j], 0.0f, j, n, lane, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        gate[j][e] *= p.residual_scale;
+        scale[j][e] = (1.0f + scale[j][e]) * wpre[j][e];
+        sum_n[j][e] = sum_z[j][e] = sum_h[j][e] = 0.0f;
+      }
+    }
+    // Every slot takes part in every barrier; a slot past the end repeats the
+    // last row without adding or writing it.
+    if (start + slot < end) fetch(start + slot);
+    else fetch(end - 1);
+    for (int64_t first = start; first < end; first += p.slots) {
+      const int64_t row = first + slot;
+      const bool live = row < end;
+      const float4 st = in_stats;
+      float dr[NCH][8], dh[NCH][8], x[NCH][8], z[NCH][8];
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dr[j][e] = has_dr ? in_dr[j][e] : 0.0f;
+          dh[j][e] = has_h ? in_dh[j][e] : 0.0f;
+          // Lanes past the end hold 0, not -mean.
+          x[j][e] = has_h && inside<WIDE>(j, e, n, lane, c) ? (in_r[j][e] - st.x) * st.y : 0.0f;
+          z[j][e] = has_y ? in_y[j][e] : 0.0f;
+        }
+      if (row + p.slots < end) fetch(row + p.slots);
+      if (has_h) {
+        float g[NCH][8];
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            g[j][e] = dh[j][e] * scale[j][e];
+            if (live) {
+              sum_n[j][e] = __builtin_fmaf(dh[j][e], x[j][e], sum_n[j][e]);
+              sum_h[j][e] += dh[j][e];
+            }
+          }
+        through_norm<NCH>(g, x, p.pre == TERN_NORM_LAYER, st.y, c, sums);
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dr[j][e] += g[j][e];
+      }
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+          store_piece<WIDE>(static_cast<RT*>(p.dr) + row * p.lddr, dr[j], j, n, lane, c);
+      }
+      if (has_y) {
+        float g[NCH][8];
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool in = inside<WIDE>(j, e, n, lane, c);
+            if (!in) dr[j][e] = 0.0f;
+            if (p.post != TERN_NORM_NONE) z[j][e] = in ? (z[j][e] - st.z) * st.w : 0.0f;
+            g[j][e] = gate[j][e] * wpost[j][e] * dr[j][e];
+            if (live) sum_z[j][e] = __builtin_fmaf(dr[j][e], z[j][e], sum_z[j][e]);
+          }
+        if (p.post != TERN_NORM_NONE)
+          through_norm<NCH>(g, z, p.post == TERN_NORM_LAYER, st.w, c, sums);
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < NCH; ++j)
+            store_piece<WIDE>(static_cast<bf16*>(p.dy) + row * p.lddy, g[j], j, n, lane, c);
+        }
+      }
+    }
+    if (p.part != nullptr) {
+      // The slots' sums, added in the slots' order.
+      for (int k = 1; k < p.slots; ++k) {
+        __syncthreads();
+        if (slot == k) {
+#pragma unroll
+          for (int j = 0; j < NCH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              joined[(8 * j + e) * n + lane] = sum_n[j][e];
+              joined[(8 * (NCH + j) + e) * n + lane] = sum_z[j][e];
+              joined[(8 * (2 * NCH + j) + e) * n + lane] = sum_h[j][e];
+            }
+        }
+        __syncthreads();
+        if (slot == 0) {
+#pragma unroll
+          for (int j = 0; j < NCH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              sum_n[j][e] += joined[(8 * j + e) * n + lane];
+              sum_z[j][e] += joined[(8 * (NCH + j) + e) * n + lane];
+              sum_h[j][e] += joined[(8 * (2 * NCH + j) + e) * n + lane];
+            }
+        }
+      }
+      if (slot == 0) {
+        float* out = p.part + (static_cast<int64_t>(blockIdx.x) + sample) * 3 * c;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+          store_piece<WIDE>(out, sum_n[j], j, n, lane, c);
+          store_piece<WIDE>(out + c, sum_z[j], j, n, lane, c);
+          store_piece<WIDE>(out + 2 * c, sum_h[j], j, n, lane, c);
+        }
+      }
+    }
+    start = end;
+  }
+}
+
+constexpr int kSumLanes = 8;  // partials read side by side for one channel
+
+// A sample's partials, added: 64 channels a workgroup, kSumLanes partials at a
+// time, then the lanes in order.
+__global__ __launch_bounds__(64 * kSumLanes) void residual_norm_sums_kernel(
+    ResidualNormBwdParams p) {
+  __shared__ float part[3][kSumLanes][64];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
+  for (int64_t sample = blockIdx.y; sample < p.samples; sample += gridDim.y) {
+    const int64_t begin = sample * p.tokens;
+    const int64_t end = begin + p.tokens < p.m ? begin + p.tokens : p.m;
+    const int64_t w1 = (end - 1) / p.rows;
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    if (col < p.c) {
+      for (int64_t w = begin / p.rows + k; w <= w1; w += kSumLanes) {
+        const float* in = p.part + (w + sample) * 3 * p.c + col;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) s[i] += in[static_cast<int64_t>(i) * p.c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) part[i][k][threadIdx.x & 63] = s[i];
+    __syncthreads();
+    if (k < 3) {  // wave i adds up and writes sum i
+      float t = 0.0f;
+#pragma unroll
+      for (int l = 0; l < kSumLanes; ++l) t += part[k][l][threadIdx.x & 63];
+      if (col < p.c) {
+        const int64_t at = sample * p.c + col;
+        if (k == 0) {
+          if (p.dscale) p.dscale[at] = t * (p.pre_weight ? p.pre_weight[col] : 1.0f);
+          if (p.dpre_weight)
+            p.totals[at] = t * (1.0f + (p.scale ? p.scale[sample * p.ldscale + col] : 0.0f));
+        } else if (k == 1) {
+          const float a = p.residual_scale * t;
+          if (p.dgate) p.dgate[at] = a * (p.post_weight ? p.post_weight[col] : 1.0f);
+          if (p.dpost_weight)
+            p.totals[(p.samples + sample) * p.c + col] =
+                a * (p.gate ? p.gate[sample * p.ldgate + col] : 1.0f);
+        } else if (p.dshift) {
+          p.dshift[at] = t;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The weights' gradients: the samples' shares, added; blockIdx.y picks the weight.
+__global__ __launch_bounds__(64 * kSumLanes) void residual_norm_weights_kernel(
+    ResidualNormBwdParams p) {
+  float* out = blockIdx.y ? p.dpost_weight : p.dpre_weight;
+  if (out == nullptr) return;
+  __shared__ float part[kSumLanes][64];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
+  const float* in = p.totals + static_cast<int64_t>(blockIdx.y) * p.samples * p.c;
+  float s = 0.0f;
+  if (col < p.c)
+    for (int64_t i = k; i < p.samples; i += kSumLanes) s += in[i * p.c + col];
+  part[k][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (k == 0 && col < p.c) {
+    s = 0.0f;
+#pragma unroll
+    for (int l = 0; l < kSumLanes; ++l) s += part[l][threadIdx.x & 63];
+    out[col] = s;
+  }
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// A row's waves and the channels a lane holds (8 NCH): one piece a lane up to
+// eight waves (4096 channels), then two.
+int waves_of(int c, int* pieces) {
+  const int whole = (c + 511) / 512;  // waves with one piece a lane
+  *pieces = whole <= 8 ? 1 : 2;
+  return (whole + *pieces - 1) / *pieces;
+}
+
+struct BwdPlan {
+  int pieces, waves, slots;
+  int64_t rows, groups, samples;
+};
+
+// About one workgroup of up to 12 waves a CU: each leaves a triple of partial
+// sums a channel (12 bytes written and read) for the rows it takes, so fewer
+// workgroups with several rows side by side cost less than many.
+BwdPlan plan_bwd(int64_t m, int64_t c, int64_t tokens) {
+  BwdPlan b;
+  b.waves = waves_of(static_cast<int>(c), &b.pieces);
+  const int most = b.pieces == 1 ? 12 : 8;
+  b.slots = most / b.waves;
+  b.rows = (m + 255) / 256;
+  if (b.slots > b.rows) b.slots = static_cast<int>(b.rows);
+  if (b.slots > tokens) b.slots = static_cast<int>(tokens);
+  b.groups = (m + b.rows - 1) / b.rows;
+  b.samples = (m + tokens - 1) / tokens;
+  return b;
+}
+
+template <typename RT, bool WIDE>
+hipError_t launch_fwd(ResidualNormParams& p, int pieces, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((p.m + p.rows - 1) / p.rows)), block(p.threads);
+  if (pieces == 1)
+    hipLaunchKernelGGL((residual_norm_kernel<RT, 1, WIDE>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((residual_norm_kernel<RT, 2, WIDE>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+template <typename RT, bool WIDE>
+hipError_t launch_bwd(ResidualNormBwdParams& p, const BwdPlan& b, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(b.groups)), block(p.threads * b.slots);
+  const unsigned lds = b.slots > 1 ? 3u * 8u * b.pieces * p.threads * 4u : 0u;
+  if (b.pieces == 1)
+    hipLaunchKernelGGL((residual_norm_bwd_kernel<RT, 1, WIDE>), grid, block, lds, stream, p);
+  else
+    hipLaunchKernelGGL((residual_norm_bwd_kernel<RT, 2, WIDE>), grid, block, lds, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_residual_norm(ResidualNormParams& p, bool r_is_bf16, hipStream_t stream) {
+  int pieces;
+  const int waves = waves_of(p.c, &pieces);
+  p.threads = 64 * waves;
+  // Rows a workgroup walks over: enough workgroups for about 24 waves a CU,
+  // at most 8 rows (past that the sample's vectors cost nothing more).
+  int64_t rows = p.m * waves / (256 * 24);
+  p.rows = rows < 1 ? 1 : rows > 8 ? 8 : rows;
+  const bool wide = p.c % 8 == 0 && p.ldr % 8 == 0 && aligned16(p.r) && p.ldy % 8 == 0 &&
+                    aligned16(p.y) && p.ldro % 8 == 0 && aligned16(p.r_out) && p.ldh % 8 == 0 &&
+                    aligned16(p.h) && aligned16(p.pre_weight) && aligned16(p.post_weight) &&
+                    aligned16(p.gate) && p.ldgate % 4 == 0 && aligned16(p.scale) &&
+                    p.ldscale % 4 == 0 && aligned16(p.shift) && p.ldshift % 4 == 0;
+  if (r_is_bf16)
+    return wide ? launch_fwd<bf16, true>(p, pieces, stream) : launch_fwd<bf16, false>(p, pieces, stream);
+  return wide ? launch_fwd<float, true>(p, pieces, stream) : launch_fwd<float, false>(p, pieces, stream);
+}
+
+int64_t residual_norm_bwd_workspace(int64_t m, int64_t c, int64_t tokens) {
+  if (m == 0) return 0;
+  const BwdPlan b = plan_bwd(m, c, tokens);
+  // Partials of every (workgroup, sample) and the samples' shares of the two weights,
+  // the second part from a 16-byte boundary.
+  return ((b.groups + b.samples) * 3 * c + 3 + 2 * b.samples * c) * 4;
+}
+
+hipError_t launch_residual_norm_bwd(ResidualNormBwdParams& p, bool r_is_bf16, void* workspace,
+                                    hipStream_t stream) {
+  if (p.m == 0) {
+    p.samples = 0;
+    if (p.dpre_weight || p.dpost_weight)
+      hipLaunchKernelGGL(residual_norm_weights_kernel, dim3((p.c + 63) / 64, 2),
+                         dim3(64 * kSumLanes), 0, stream, p);
+    return hipGetLastError();
+  }
+  const BwdPlan b = plan_bwd(p.m, p.c, p.tokens);
+  p.threads = 64 * b.waves;
+  p.slots = b.slots;
+  p.rows = b.rows;
+  p.samples = b.samples;
+  const bool sums = p.dgate || p.dscale || p.dshift || p.dpre_weight || p.dpost_weight;
+  p.part = sums ? static_cast<float*>(workspace) : nullptr;
+  p.totals = static_cast<float*>(workspace) + ((b.groups + b.samples) * 3 * p.c + 3) / 4 * 4;
+  const bool wide = p.c % 8 == 0 && p.lddro % 8 == 0 && aligned16(p.dr_out) && p.lddh % 8 == 0 &&
+                    aligned16(p.dh) && p.ldro % 8 == 0 && aligned16(p.r_out) && p.ldy % 8 == 0 &&
+                    aligned16(p.y) && p.lddr % 8 == 0 && aligned16(p.dr) && p.lddy % 8 == 0 &&
+                    aligned16(p.dy) && aligned16(p.pre_weight) && aligned16(p.post_weight) &&
+                    aligned16(p.gate) && p.ldgate % 4 == 0 && aligned16(p.scale) &&
+                    p.ldscale % 4 == 0;
+  hipError_t e;
+  if (r_is_bf16)
+    e = wide ? launch_bwd<bf16, true>(p, b, stream) : launch_bwd<bf16, false>(p, b, stream);
+  else
+    e = wide ? launch_bwd<float, true>(p, b, stream) : launch_bwd<float, false>(p, b, stream);
+  if (e != hipSuccess || !sums) return e;
+  const unsigned cols = static_cast<unsigned>((p.c + 63) / 64);
+  const unsigned samples = static_cast<unsigned>(p.samples < 65535 ? p.samples : 65535);
+  hipLaunchKernelGGL(residual_norm_sums_kernel, dim3(cols, samples), dim3(64 * kSumLanes), 0,
+                     stream, p);
+  e = hipGetLastError();
+  if (e != hipSuccess || !(p.dpre_weight || p.dpost_weight)) return e;
+  hipLaunchKernelGGL(residual_norm_weights_kernel, dim3(cols, 2), dim3(64 * kSumLanes), 0, stream,
+                     p);
+  return hipGetLastError();
+}
+
+}  // namespace tern

@@ -1,0 +1,183 @@
+// Rotary positions with several axes (time, height, width, ...).
+//
+// The first 2P channels of every head are P pairs (u, v).  Each axis owns a
+// run of pairs; pair i of an axis of width w turns by
+//   angle = pos[axis] * theta^(-2 i / w):  (u, v) -> (u c - v s, u s + v c),
+// or by -angle for the transpose (the backward pass).  Channels past 2P pass
+// unchanged.
+//
+// Bound by memory: each element is read once and written once.  One thread
+// holds the cosines and sines of a few pairs of one token and walks over
+// heads with them, so the angles cost a few instructions an element and no
+// table is read; consecutive threads hold consecutive pairs, then heads, so a
+// wave reads whole lines.
+// The angle is taken in turns: turn = theta^(-2i/w) / (2 pi) comes as an fp32
+// head and tail (48 bits), the product with the position keeps its rounding
+// error through one fma, and only then whole turns are dropped.  The angle
+// is therefore right to about 2^-24 turns for positions up to 2^24, where an fp32
+// product alone would lose a bit for every doubling of the position.
+// 4608 tokens x 48 heads of 128 in bf16 (113 MB): see the figures at the launch.
+#include "internal.h"
+
+namespace tern {
+namespace {
+
+template <typename T, int N>
+using vec_t = __attribute__((ext_vector_type(N))) T;
+
+// N consecutive elements, aligned to N elements (WIDE), or the first `have` of
+// them one at a time.
+template <bool WIDE, typename T, int N>
+__device__ inline void load_run(const T* p, float (&f)[N], int have) {
+  if constexpr (WIDE) {
+    const vec_t<T, N> v = *reinterpret_cast<const vec_t<T, N>*>(p);
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = static_cast<float>(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = e < have ? static_cast<float>(p[e]) : 0.0f;
+  }
+}
+
+template <bool WIDE, typename T, int N>
+__device__ inline void store_run(T* p, const float (&f)[N], int have) {
+  if constexpr (WIDE) {
+    vec_t<T, N> v;
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = static_cast<T>(f[e]);
+    *reinterpret_cast<vec_t<T, N>*>(p) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < have) p[e] = static_cast<T>(f[e]);
+  }
+}
+
+// at * (hi + lo) less its whole turns.  The compiler must not fuse the first
+// product into the subtraction: its rounding error would be counted twice.
+__device__ inline float part_of_a_turn(float at, float hi, float lo) {
+#pragma clang fp contract(off)
+  const float whole = at * hi;
+  const float err = __builtin_fmaf(at, hi, -whole) + at * lo;
+  return (whole - rintf(whole)) + err;
+}
+
+// VP pairs per thread.  Interleaved layout: channels 2p, 2p + 1 (one run of
+// 2 VP channels a thread); halves: channels p, p + P (two runs of VP).  Work
+// item: unit (fastest), head lane, token; the item's heads are lane,
+// lane + lanes, ...  blockIdx.y is the batch.
+template <typename T, int VP, bool HALVES, bool WIDE, int HEADS>
+__global__ __launch_bounds__(256) void rope_kernel(RopeParams a) {
+  const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+  if (item >= a.items) return;
+  const uint32_t units = a.turn_units + a.rest_units;
+  const uint32_t rest = item / units, u = item - rest * units;
+  const uint32_t t = rest / a.lanes, lane = rest - t * a.lanes;
+  const int64_t b = blockIdx.y;
+  const T* x = static_cast<const T*>(a.x.data) + b * a.x.batch + t * a.x.token;
+  T* y = static_cast<T*>(a.y.data) + b * a.y.batch + t * a.y.token;
+
+  constexpr int kRun = HALVES ? VP : 2 * VP;
+  const bool turns = u < a.turn_units;
+  // First channels of this unit's runs, and how many channels each has.
+  int c0, c1 = 0, n0 = kRun, n1 = 0;
+  float cs[VP], sn[VP];
+  if (turns) {
+    const int p0 = static_cast<int>(u) * VP;
+    c0 = HALVES ? p0 : 2 * p0;
+    if (HALVES) {
+      c1 = a.pairs + p0;
+      n1 = kRun;
+    }
+    const float* pos = a.pos + b * a.pos_batch + t * a.pos_token;
+#pragma unroll
+    for (int e = 0; e < VP; ++e) {
+      const int p = p0 + e;
+      const int axis = (p >= a.first[0]) + (p >= a.first[1]) + (p >= a.first[2]);
+      sincospif(2.0f * part_of_a_turn(pos[axis], a.turn[p], a.turn_tail[p]), &sn[e], &cs[e]);
+      if (a.inverse) sn[e] = -sn[e];
+    }
+  } else {
+    c0 = 2 * a.pairs + static_cast<int>(u - a.turn_units) * (2 * VP);
+    n0 = a.d - c0 < kRun ? a.d - c0 : kRun;
+    if (HALVES) {
+      c1 = c0 + kRun;
+      n1 = a.d - c1 < kRun ? a.d - c1 : kRun;
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < HEADS; ++g) {
+    const uint32_t h = lane + g * a.lanes;
+    if (h >= a.h) break;
+    const T* xh = x + h * a.x.head;
+    T* yh = y + h * a.y.head;
+    float p[kRun], q[kRun];
+    load_run<WIDE>(xh + c0, p, n0);
+    if (HALVES && n1 > 0) load_run<WIDE>(xh + c1, q, n1);
+    if (turns) {
+#pragma unroll
+      for (int e = 0; e < VP; ++e) {
+        float& v0 = HALVES ? p[e] : p[2 * e];
+        float& v1 = HALVES ? q[e] : p[2 * e + 1];
+        const float s = v0, r = v1;
+        v0 = __builtin_fmaf(s, cs[e], -(r * sn[e]));
+        v1 = __builtin_fmaf(s, sn[e], r * cs[e]);
+      }
+    }
+    store_run<WIDE>(yh + c0, p, n0);
+    if (HALVES && n1 > 0) store_run<WIDE>(yh + c1, q, n1);
+  }
+}
+
+template <typename T, int VP, bool HALVES, bool WIDE>
+hipError_t launch(RopeParams& a, int64_t b, int64_t t, hipStream_t stream) {
+  a.turn_units = (a.pairs + VP - 1) / VP;
+  a.rest_units = (a.d - 2 * a.pairs + 2 * VP - 1) / (2 * VP);
+  const int64_t units = a.turn_units + a.rest_units;
+  // Four heads a thread where that leaves enough threads to fill the chip.
+  const int64_t quarter = (static_cast<int64_t>(a.h) + 3) / 4;
+  const bool four = b * t * units * quarter >= (int64_t(1) << 17);
+  a.lanes = static_cast<uint32_t>(four ? quarter : a.h);
+  a.items = static_cast<uint32_t>(t * units * a.lanes);
+  const dim3 grid((a.items + 255u) / 256u, static_cast<unsigned>(b));
+  if (four)
+    hipLaunchKernelGGL((rope_kernel<T, VP, HALVES, WIDE, 4>), grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((rope_kernel<T, VP, HALVES, WIDE, 1>), grid, dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+// Whether every run of n elements that a unit of this width reads or writes
+// starts at a multiple of n elements and is whole.
+bool wide(const RopeParams& a, int n, int size) {
+  auto fits = [&](const tern_heads& v) {
+    return reinterpret_cast<uintptr_t>(v.data) % static_cast<uintptr_t>(n * size) == 0 &&
+           v.batch % n == 0 && v.token % n == 0 && v.head % n == 0;
+  };
+  return a.d % n == 0 && fits(a.x) && fits(a.y);
+}
+
+}  // namespace
+
+hipError_t launch_rope(RopeParams& a, bool is_bf16, bool halves, int64_t b, int64_t t,
+                       hipStream_t stream) {
+  if (is_bf16) {
+    if (halves) {
+      if (a.pairs % 8 == 0 && wide(a, 8, 2))
+        return launch<__bf16, 8, true, true>(a, b, t, stream);
+      if (a.pairs % 4 == 0 && wide(a, 4, 2))
+        return launch<__bf16, 4, true, true>(a, b, t, stream);
+      return launch<__bf16, 1, true, false>(a, b, t, stream);
+    }
+    if (a.pairs % 4 == 0 && wide(a, 8, 2)) return launch<__bf16, 4, false, true>(a, b, t, stream);
+    return launch<__bf16, 1, false, false>(a, b, t, stream);
+  }
+  if (halves) {
+    if (a.pairs % 4 == 0 && wide(a, 4, 4)) return launch<float, 4, true, true>(a, b, t, stream);
+    return launch<float, 1, true, false>(a, b, t, stream);
+  }
+  if (a.pairs % 2 == 0 && wide(a, 4, 4)) return launch<float, 2, false, true>(a, b, t, stream);
+  return launch<float, 1, false, false>(a, b, t, stream);
+}
+
+}  // namespace tern

@@ -1,0 +1,298 @@
+"""The boundary between two blocks (tern_residual_norm and its gradients)
+against the formulas in 64 bits.
+
+Tolerances, fixed by the arithmetic.  r_out is one fp32 product chain and a sum:
+2^-21 of its terms' size, plus one rounding to bf16 (2^-8 relative) for a bf16
+stream.  Everything after it is checked from the stored r_out (and the backward
+pass from the stored statistics), so no rounding of the stream enters twice.  A
+row's statistics are fp32 sums of c terms in a tree (8 or 16 in a lane, 64 lanes, up
+to 8 waves: under 32 roundings in sequence), relative 2^-18 with room; bf16 outputs
+have one rounding more.  A sum over rows of m terms goes through at most m
+roundings in sequence: m 2^-23 of the sum of the terms' sizes, and the terms carry 2^-18.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from parity import DEV, log
+
+pytestmark = pytest.mark.gpu
+tern = pytest.importorskip("ternary_weight_quantized_tern_amd")
+
+F32 = 2.0 ** -18
+BF16 = 2.0 ** -8
+
+
+def stats_ref(x, kind, eps):
+    mean = x.mean(1, keepdim=True) if kind == "layer" else torch.zeros_like(x[:, :1])
+    return mean, 1.0 / torch.sqrt(((x - mean) ** 2).mean(1, keepdim=True) + eps)
+
+
+def each(v, m, tokens, none):
+    if v is None:
+        return none
+    return v.double()[torch.arange(m, device=v.device) // tokens]
+
+
+def or_one(w):
+    return 1.0 if w is None else w.double()
+
+
+def near(got, ref, size, rel, what):
+    off = (got.double() - ref).abs()
+    bound = rel * ref.abs() + size
+    assert bool(torch.isfinite(got).all()), what
+    assert bool((off <= bound).all()), (what, float((off - bound).max()))
+
+
+def make(m, c, tokens, dtype, weights, seed, pitch=0, offset=0.3):
+    g = torch.Generator().manual_seed(seed)
+    samples = -(-m // tokens)
+
+    def rows(dt):
+        return torch.randn(m, c + pitch, generator=g).to(dt).to(DEV)[:, :c]
+
+    r = (rows(torch.float32) + offset).to(dtype)
+    if pitch:
+        r = torch.cat([r, r[:, :pitch]], 1)[:, :c]
+    y = rows(torch.bfloat16)
+    mod = (0.3 * torch.randn(samples, 3 * c, generator=g)).to(DEV)
+    shift, scale, gate = mod.split(c, 1)
+    w = [1 + 0.1 * torch.randn(c, generator=g).to(DEV) for _ in range(2)]
+    dr_out, dh = rows(torch.float32).to(dtype), rows(torch.bfloat16)
+    return r, y, gate, scale, shift, (w if weights else [None, None]), dr_out, dh
+
+
+CASES = [
+    # m, c, tokens, dtype, pre, post, weights, pitch
+    (1, 8, 1, torch.float32, "layer", None, False, 0),
+    (8, 1152, 1, torch.bfloat16, "layer", None, False, 0),
+    (37, 1152, 10, torch.bfloat16, "rms", "rms", True, 0),    # a last sample of 7 rows
+    (300, 1152, 100, torch.float32, "layer", "layer", True, 8),
+    (520, 64, 130, torch.float32, "rms", None, True, 0),
+    (65, 513, 65, torch.bfloat16, "layer", "rms", True, 0),   # an odd width
+    (50, 63, 7, torch.float32, "layer", "layer", False, 3),   # an odd pitch
+    (700, 3072, 700, torch.bfloat16, "layer", None, False, 0),
+    (33, 4100, 11, torch.bfloat16, "rms", "layer", False, 0),  # two pieces a lane, not wide
+    (19, 8192, 19, torch.float32, "layer", "rms", True, 0),
+    (1100, 256, 3, torch.bfloat16, "layer", None, True, 0),   # more samples than workgroups
+    (600, 1, 600, torch.float32, "rms", None, False, 0),
+]
+
+
+@pytest.mark.parametrize("m,c,tokens,dtype,pre,post,weights,pitch", CASES)
+def test_forward_and_backward_match_the_formulas(m, c, tokens, dtype, pre, post, weights, pitch):
+    log(f"residual_norm m={m} c={c} tokens={tokens} {dtype} {pre} {post} {weights} {pitch}")
+    r, y, gate, scale, shift, (wpre, wpost), dr_out, dh = make(m, c, tokens, dtype, weights,
+                                                               m + c + tokens, pitch)
+    if post is None:
+        wpost = None
+    eps, alpha = 1e-5, 0.75
+    opt = dict(tokens=tokens, pre=pre, post=post, pre_weight=wpre, post_weight=wpost,
+               residual_scale=alpha, eps=eps)
+    r_out, h, stats = tern.residual_norm(r, y, gate=gate, scale=scale, shift=shift,
+                                         with_stats=True, **opt)
+    torch.cuda.synchronize()
+    low = BF16 if dtype == torch.bfloat16 else 0.0
+
+    z = y.double()
+    zmean, zrstd = torch.zeros_like(z[:, :1]), torch.zeros_like(z[:, :1])
+    if post:
+        zmean, zrstd = stats_ref(z, post, eps)
+        z = (z - zmean) * zrstd * or_one(wpost)
+    g = each(gate, m, tokens, 1.0)
+    step = alpha * g * z
+    near(r_out, r.double() + step, F32 * (r.double().abs() + step.abs() + 1e-3), low, "r_out")
+    x = r_out.double()
+    mean, rstd = stats_ref(x, pre, eps)
+    top = x.abs().amax(1, keepdim=True)
+    n = (x - mean) * rstd * or_one(wpre)
+    s1 = 1 + each(scale, m, tokens, 0.0)
+    sh = each(shift, m, tokens, 0.0)
+    hsize = F32 * ((top + mean.abs()) * rstd * (s1.abs() if torch.is_tensor(s1) else 1) * 1.5 + sh.abs())
+    near(h, n * s1 + sh, hsize, BF16, "h")
+    near(stats[:, 0:1], mean, F32 * top, 0.0, "mean")
+    near(stats[:, 1:2], rstd, 0.0, F32 * 4, "rstd")
+    near(stats[:, 2:3], zmean, F32 * y.double().abs().amax(1, keepdim=True), 0.0, "post mean")
+    near(stats[:, 3:4], zrstd, 0.0, F32 * 4, "post rstd")
+
+    # backward, from the stored values
+    got = tern.residual_norm_backward(dr_out, dh, r_out, y, stats, gate=gate, scale=scale, **opt)
+    again = tern.residual_norm_backward(dr_out, dh, r_out, y, stats, gate=gate, scale=scale, **opt)
+    torch.cuda.synchronize()
+    for a, b in zip(got, again):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+    dr, dy, dgate, dscale, dshift, dpre, dpost = got
+    mean, rstd, zmean, zrstd = (stats[:, i:i + 1].double() for i in range(4))
+    nx = (x - mean) * rstd
+
+    def through(gr, xn, rs, kind):
+        out = gr - xn * (gr * xn).mean(1, keepdim=True)
+        if kind == "layer":
+            out = out - gr.mean(1, keepdim=True)
+        size = (gr.abs() + xn.abs() * (gr * xn).abs().mean(1, keepdim=True)
+                + gr.abs().mean(1, keepdim=True)) * rs
+        return out * rs, size
+
+    dhd = dh.double()
+    inner, isize = through(dhd * s1 * or_one(wpre), nx, rstd, pre)
+    drf = dr_out.double() + inner
+    dsize = F32 * (dr_out.double().abs() + isize)
+    near(dr, drf, dsize, low, "dr")
+    zn = (y.double() - zmean) * zrstd if post else y.double()
+    dz = alpha * g * drf
+    if post:
+        dyf, ysize = through(dz * or_one(wpost), zn, zrstd, post)
+        # dr's own error goes through the same linear map
+        _, grown = through((alpha * g * dsize * or_one(wpost)).abs(), zn.abs(), zrstd, "rms")
+    else:
+        dyf, ysize, grown = dz, dz.abs(), (alpha * g * dsize).abs()
+    near(dy, dyf, F32 * ysize + grown, BF16, "dy")
+
+    def by_sample(t):
+        return torch.stack([p.sum(0) for p in t.split(tokens)])
+
+    rel = F32 + min(m, tokens) * 2.0 ** -23
+    zfull = zn * or_one(wpost)
+    near(dgate, alpha * by_sample(drf * zfull),
+         rel * by_sample((drf * zfull).abs()) + by_sample(dsize * zfull.abs()) + 1e-30, 0.0, "dgate")
+    near(dscale, by_sample(dhd * nx * or_one(wpre)),
+         rel * by_sample((dhd * nx * or_one(wpre)).abs()) + 1e-30, 0.0, "dscale")
+    near(dshift, by_sample(dhd), rel * by_sample(dhd.abs()) + 1e-30, 0.0, "dshift")
+    relw = F32 + m * 2.0 ** -23
+    if weights:
+        t = dhd * s1 * nx
+        near(dpre, t.sum(0), relw * t.abs().sum(0) + 1e-30, 0.0, "dpre_weight")
+    else:
+        assert dpre is None
+    if weights and post:
+        t = dz * zn
+        near(dpost, t.sum(0), relw * t.abs().sum(0) + (alpha * g * dsize * zn).abs().sum(0) + 1e-30,
+             0.0, "dpost_weight")
+    else:
+        assert dpost is None
+
+
+def test_parts_left_out():
+    log("residual_norm parts")
+    m, c, tokens = 70, 264, 35
+    r, y, gate, scale, shift, (wpre, wpost), dr_out, dh = make(m, c, tokens, torch.float32, True, 3)
+    # no branch: the first norm of a stack
+    same, h, st = tern.residual_norm(r, scale=scale, shift=shift, tokens=tokens, with_stats=True)
+    assert same is r
+    mean, rstd = stats_ref(r.double(), "layer", 1e-6)
+    ref = (r.double() - mean) * rstd * (1 + each(scale, m, tokens, 0)) + each(shift, m, tokens, 0)
+    near(h, ref, F32 * 40, BF16, "h without y")
+    dr, dy, dgate, dscale, dshift, dpre, dpost = tern.residual_norm_backward(
+        None, dh, r, None, st, scale=scale, tokens=tokens)
+    assert dy is None and dgate is None and dpre is None and dpost is None
+    near(dshift, torch.stack([p.sum(0) for p in dh.double().split(tokens)]), 1e-3, 0.0, "dshift")
+    # no following norm: the last residual of a stack, in place
+    r2 = r.clone()
+    r_out, none = tern.residual_norm(r2, y, gate=gate, tokens=tokens, pre=None)
+    assert none is None
+    near(r_out, r.double() + each(gate, m, tokens, 1) * y.double(), F32 * 8, 0.0, "gate only")
+    dr, dy, dgate, dscale, dshift, _, _ = tern.residual_norm_backward(
+        dr_out, None, r_out, y, torch.zeros(m, 4, device=DEV), gate=gate, tokens=tokens, pre=None)
+    assert torch.equal(dr, dr_out) and dscale is None and dshift is None
+    near(dy, each(gate, m, tokens, 1) * dr_out.double(), F32 * 8, BF16, "dy gate only")
+    # nothing but the norm of a sum
+    r_out, h = tern.residual_norm(r, y)
+    mean, rstd = stats_ref(r_out.double(), "layer", 1e-6)
+    near(h, (r_out.double() - mean) * rstd, F32 * 40, BF16, "plain")
+    # no rows
+    e, eh = tern.residual_norm(r[:0], y[:0])
+    assert e.shape == (0, c) and eh.shape == (0, c)
+    out = tern.residual_norm_backward(r[:0], dh[:0], r[:0], y[:0], torch.zeros(0, 4, device=DEV),
+                                      pre_weight=wpre, post="rms", post_weight=wpost)
+    assert float(out[5].abs().sum()) == 0.0 and float(out[6].abs().sum()) == 0.0
+
+
+def test_a_large_mean_keeps_the_variance():
+    # mean 1000, deviation 1: squares about zero in fp32 would leave 6 % of the variance
+    g = torch.Generator().manual_seed(5)
+    r = (1000 + torch.randn(40, 1152, generator=g)).to(DEV)
+    _, h, st = tern.residual_norm(r, with_stats=True)
+    mean, rstd = stats_ref(r.double(), "layer", 1e-6)
+    # the centred values carry the fp32 spacing of the mean, 2^-14
+    near(st[:, 1:2], rstd, 0.0, 1e-3, "rstd")
+    near(h, (r.double() - mean) * rstd, 2e-3, BF16, "h")
+
+
+def test_constant_rows_and_zero_eps():
+    r = torch.full((3, 128), 2.5, device=DEV)
+    _, h = tern.residual_norm(r)
+    assert float(h.float().abs().max()) == 0.0
+    _, h, st = tern.residual_norm(torch.full((3, 128), 2.0, device=DEV), pre="rms", eps=0.0,
+                                  with_stats=True)
+    assert bool((h == 1).all()) and bool((st[:, 1] == 0.5).all())
+
+
+def test_autograd_matches_differences():
+    g = torch.Generator().manual_seed(6)
+    m, c, tokens = 24, 96, 12
+    r = torch.randn(m, c, generator=g).to(DEV).requires_grad_()
+    y = torch.randn(m, c, generator=g).to(torch.bfloat16).to(DEV).requires_grad_()
+    vec = [(0.3 * torch.randn(2, c, generator=g)).to(DEV).requires_grad_() for _ in range(3)]
+    w = [(1 + 0.1 * torch.randn(c, generator=g)).to(DEV).requires_grad_() for _ in range(2)]
+    a = torch.randn(m, c, generator=g).to(DEV)
+    b = torch.randn(m, c, generator=g).to(torch.bfloat16).to(DEV)
+
+    def f(*t):
+        return tern.block_boundary(t[0], t[1], gate=t[2], scale=t[3], shift=t[4], pre_weight=t[5],
+                                   post_weight=t[6], tokens=tokens, pre="layer", post="rms")
+
+    args = [r, y, *vec, *w]
+    ro, h = f(*args)
+    torch.autograd.backward([ro, h], [a, b])
+
+    def plain(t):  # the same function in 64 bits
+        z = t[1]
+        z = z / torch.sqrt((z * z).mean(1, keepdim=True) + 1e-6) * t[6]
+        rep = lambda v: v.repeat_interleave(tokens, 0)  # noqa: E731
+        x = t[0] + rep(t[2]) * z
+        mean, rstd = stats_ref(x, "layer", 1e-6)
+        hh = (x - mean) * rstd * t[5] * (1 + rep(t[3])) + rep(t[4])
+        return (x * a.double()).sum() + (hh * b.double()).sum()
+
+    base = [t.detach().double() for t in args]
+    for i, t in enumerate(args):
+        v = torch.randn(t.shape, generator=g).to(DEV).double()
+        step = 1e-5
+        up, down = list(base), list(base)
+        up[i] = base[i] + step * v
+        down[i] = base[i] - step * v
+        diff = float(plain(up) - plain(down)) / (2 * step)
+        along = float((t.grad.double() * v).sum())
+        # bf16 gradients are within 2^-8 of themselves, element by element
+        room = float((t.grad.double().abs() * v.abs()).sum()) * (
+            2.0 ** -8 if t.dtype == torch.bfloat16 else 2.0 ** -14) + 1e-3
+        assert abs(diff - along) <= room, (i, diff, along)
+
+
+def test_refusals():
+    r = torch.zeros(4, 16, device=DEV)
+    y = torch.zeros(4, 16, device=DEV, dtype=torch.bfloat16)
+    st = torch.zeros(4, 4, device=DEV)
+    w = torch.ones(16, device=DEV)
+    for bad in (lambda: tern.residual_norm(r, pre=None),               # nothing to compute
+                lambda: tern.residual_norm(r, y, post_weight=w),       # a weight without its norm
+                lambda: tern.residual_norm(r, y, eps=-1.0),
+                lambda: tern.residual_norm(torch.zeros(2, 8200, device=DEV)),
+                lambda: tern.residual_norm_backward(None, None, r, y, st)):
+        with pytest.raises(tern.TernError):
+            bad()
+    for bad in (lambda: tern.residual_norm(r.half()), lambda: tern.residual_norm(r, y.float()),
+                lambda: tern.residual_norm(r.cpu()),
+                lambda: tern.residual_norm(r, y, gate=torch.zeros(1, 16, device=DEV).bfloat16()),
+                lambda: tern.residual_norm_backward(r.bfloat16(), None, r, y, st)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: tern.residual_norm(r, y[:3]), lambda: tern.residual_norm(r.T),
+                lambda: tern.residual_norm(r, y, gate=torch.zeros(2, 16, device=DEV)),
+                lambda: tern.residual_norm(r, pre="batch"), lambda: tern.residual_norm(r, tokens=0),
+                lambda: tern.residual_norm(r, pre_weight=w[:8]),
+                lambda: tern.residual_norm_backward(r, None, r, y, st[:, :3])):
+        with pytest.raises(ValueError):
+            bad()

@@ -1,0 +1,146 @@
+"""Rotary positions with several axes (tern_rope) against the definition in 64
+bits.
+
+Tolerance, fixed by the arithmetic: the angle is exact to 2^-24 of a turn for
+these positions, so its cosine and sine are within 2 pi 2^-24 plus two units of
+fp32 rounding (2^-23), under 2^-20 in all; each output is two products and a sum
+of such values, so it is within 2^-19 (|u| + |v|) in fp32, and in bf16 one
+rounding (2^-8 relative at most) more.
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from parity import DEV, log
+
+pytestmark = pytest.mark.gpu
+tern = pytest.importorskip("ternary_weight_quantized_tern_amd")
+
+
+def reference(x, pos, axes, theta, layout, inverse):
+    """y and |u| + |v| of each channel (0 for copied ones), in 64 bits."""
+    x = x.double()
+    y, size = x.clone(), torch.zeros_like(x)
+    half = sum(axes) // 2
+    pair = 0
+    for axis, width in enumerate(axes):
+        for i in range(width // 2):
+            angle = pos[..., axis].double() * theta ** (-2.0 * i / width)
+            angle = (-angle if inverse else angle)[..., None]
+            lo, hi = (2 * pair, 2 * pair + 1) if layout == "interleaved" else (pair, pair + half)
+            u, v = x[..., lo], x[..., hi]
+            y[..., lo] = u * angle.cos() - v * angle.sin()
+            y[..., hi] = u * angle.sin() + v * angle.cos()
+            size[..., lo] = size[..., hi] = u.abs() + v.abs()
+            pair += 1
+    return y, size
+
+
+def check(y, x, pos, axes, theta, layout, inverse, what):
+    ref, size = reference(x.cpu(), pos.cpu(), axes, theta, layout, inverse)
+    bound = size * 2.0 ** -19 + (ref.abs() * 2.0 ** -8 if y.dtype == torch.bfloat16 else 0)
+    off = (y.cpu().double() - ref).abs()
+    assert bool((off <= bound).all()), (what, float((off - bound).max()))
+
+
+def inputs(b, t, h, d, n, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(b, t, h, d, generator=g).to(dtype).to(DEV)
+    pos = torch.randint(0, 300, (b, t, n), generator=g).float().to(DEV)
+    return x, pos
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "halves"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("b,t,h,d,axes", [
+    (1, 1, 1, 64, (16, 24, 24)),
+    (2, 5, 3, 72, (24, 24, 24)),
+    (1, 130, 24, 128, (16, 56, 56)),
+    (3, 33, 7, 96, (32, 32, 24)),     # the last channels pass
+    (2, 9, 5, 80, (20, 26, 30)),      # pairs that are no multiple of 4
+    (2, 3, 2, 10, (4, 2)),            # small and odd: one pair at a time
+    (1, 4, 3, 7, (6,)),               # an odd width
+    (1, 300, 40, 128, (128,)),        # one axis, several heads a thread
+    (2, 2, 2, 16, (0, 8, 0, 8)),      # axes that take no channels
+    (1, 2, 1, 256, (64, 64, 64, 64)),
+])
+def test_rope_matches_the_definition(layout, dtype, b, t, h, d, axes):
+    log(f"rope {layout} {dtype} b={b} t={t} h={h} d={d} axes={axes}")
+    x, pos = inputs(b, t, h, d, len(axes), dtype, seed=b + 3 * t + 5 * h + d)
+    for inverse in (False, True):
+        y = tern.rope(x, pos, axes, layout=layout, inverse=inverse)
+        torch.cuda.synchronize()
+        check(y, x, pos, axes, 10000.0, layout, inverse, (layout, dtype, axes, inverse))
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "halves"])
+def test_rope_views_in_place_and_shared_positions(layout):
+    log(f"rope views {layout}")
+    g = torch.Generator().manual_seed(1)
+    axes = (24, 24, 24)
+    qkv = torch.randn(2, 37, 3 * 8, 72, generator=g).to(torch.bfloat16).to(DEV)
+    pos = torch.randint(0, 50, (37, 3), generator=g).float().to(DEV)
+    keep = qkv.clone()
+    part = qkv[:, :, 8:16]  # the keys of a fused projection, turned in place
+    out = tern.rope(part, pos, axes, layout=layout, theta=500.0, out=part)
+    torch.cuda.synchronize()
+    assert out.data_ptr() == part.data_ptr()
+    check(part, keep[:, :, 8:16], pos.expand(2, 37, 3), axes, 500.0, layout, False, "in place")
+    assert torch.equal(qkv[:, :, :8], keep[:, :, :8]) and torch.equal(qkv[:, :, 16:], keep[:, :, 16:])
+    # [batch, heads, tokens, width] memory, an input broadcast over samples, and
+    # a view that starts one element off any 16-byte boundary
+    bhtd = torch.randn(1, 5, 37, 72, generator=g).to(DEV).expand(3, 5, 37, 72).transpose(1, 2)
+    check(tern.rope(bhtd, pos, axes, layout=layout), bhtd, pos.expand(3, 37, 3), axes, 1e4, layout,
+          False, "bhtd")
+    odd = torch.randn(1, 37, 5, 73, generator=g).to(DEV)[..., 1:]
+    check(tern.rope(odd, pos, axes, layout=layout), odd, pos[None], axes, 1e4, layout, False, "odd")
+
+
+def test_rope_angles_keep_their_precision_at_large_positions():
+    # At position 2^20 an fp32 product alone is off by up to 2^-4 radians.
+    axes = (64,)
+    x = torch.ones(1, 8, 1, 64, device=DEV)
+    pos = (2.0 ** 20 + torch.arange(8, device=DEV) * 12345.0)[None, :, None].contiguous()
+    check(tern.rope(x, pos, axes), x, pos, axes, 10000.0, "interleaved", False, "large")
+
+
+def test_rope_inverse_is_the_transpose_and_its_gradient():
+    x, pos = inputs(2, 19, 4, 64, 3, torch.float32, seed=3)
+    axes = (16, 24, 16)
+    back = tern.rope(tern.rope(x, pos, axes), pos, axes, inverse=True)
+    assert float((back - x).abs().max()) < 1e-5
+    g = torch.Generator().manual_seed(4)
+    dy = torch.randn(x.shape, generator=g).to(DEV)
+    xg = x.clone().requires_grad_()
+    tern.rotary(xg, pos, axes).backward(dy)
+    # linear: <dy, R(x)> = <R^T dy, x>, and a difference in a direction is exact
+    v = torch.randn(x.shape, generator=g).to(DEV)
+    diff = ((tern.rope(x + v, pos, axes) - tern.rope(x - v, pos, axes)).double() * dy).sum() / 2
+    along = (xg.grad.double() * v).sum()
+    n = x.numel()
+    assert abs(float(diff - along)) <= 1e-5 * math.sqrt(n) * 4
+
+
+def test_rope_empty_and_refusals():
+    x, pos = inputs(1, 4, 2, 16, 2, torch.float32, seed=5)
+    assert tern.rope(x[:, :0], pos[:, :0], (8, 8)).shape == (1, 0, 2, 16)
+    with pytest.raises(tern.TernError) as e:
+        tern.rope(x, pos, (8, 10))  # more channels than a head has
+    assert e.value.status == tern.TERN_ERR_ARG
+    with pytest.raises(tern.TernError):
+        tern.rope(x, pos, (7, 9))  # odd widths
+    with pytest.raises(tern.TernError):
+        tern.rope(x, pos, (8, 8), theta=0.0)
+    for bad in (lambda: tern.rope(x.half(), pos, (8, 8)), lambda: tern.rope(x, pos.int(), (8, 8)),
+                lambda: tern.rope(x.cpu(), pos, (8, 8))):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: tern.rope(x, pos[:, :3], (8, 8)), lambda: tern.rope(x, pos, (8, 4, 4)),
+                lambda: tern.rope(x[..., ::2], pos, (4, 4)),
+                lambda: tern.rope(x, pos, (8, 8), layout="pairs"),
+                lambda: tern.rope(x, pos, (8, 8), out=x[:, :, :1])):
+        with pytest.raises(ValueError):
+            bad()
