@@ -566,6 +566,58 @@ tern_status tern_residual_norm_bwd(const tern_residual_norm_args* args, const vo
  * sizes that it refuses). */
 int64_t tern_residual_norm_bwd_workspace(const tern_residual_norm_args* args);
 
+/*
+ * Attention of `queries` tokens to `keys` states of another length (an encoder's,
+ * or the same tokens), `heads` query heads on `kv_heads` key-value heads: query
+ * head j uses key-value head j / (heads / kv_heads).
+ */
+typedef struct {
+  int64_t batch;
+  int64_t queries; /* query tokens of a sample */
+  int64_t keys;    /* keys of a sample */
+  int64_t heads;
+  int64_t kv_heads; /* divides heads */
+  int64_t width;    /* channels of a head: a multiple of 8 up to TERN_ATTENTION_MAX_WIDTH */
+  float scale;      /* > 0, finite; usually 1 / sqrt(width) */
+} tern_attention_shape;
+
+#define TERN_ATTENTION_MAX_WIDTH 128
+
+/*
+ * tern_attention: for each sample b, query token t and head j
+ *   S[s] = scale * <q[b][t][j], k[b][s][j']>   over the keys s that mask keeps,
+ *   o[b][t][j] = sum_s softmax(S)[s] v[b][s][j'],   lse[b][j][t] = log sum_s exp S[s]
+ * with exact bf16 products, fp32 sums and statistics, the probabilities rounded
+ * to bf16 for the second product and one rounding of o to bf16.  A row with no
+ * kept key gives o = 0 and lse = -inf.  What memory holds at masked keys (NaN, infinities) does
+ * not matter.
+ *
+ *   q      [batch, queries, heads, width] bf16
+ *   k, v   [batch, keys, kv_heads, width] bf16
+ *   o      as q, output
+ *   mask   NULL (every key counts) or [batch, ldmask] bytes: key s of sample b
+ *          counts when mask[b * ldmask + s] != 0 (any byte alignment)
+ *   lse    [batch, heads, queries] fp32 output, natural logarithm, or NULL
+ *   workspace  at least tern_attention_workspace(shape, mask != NULL, 0) bytes, 16-byte aligned
+ *          (may be NULL when that is 0), overwritten
+ * Order of checks: scale (TERN_ERR_ARG), sizes (TERN_ERR_SHAPE): none negative,
+ * width as above, kv_heads >= 1 dividing heads (unless heads is 0), batch * heads < 2^31,
+ * queries * heads / kv_heads < 2^30, keys < 2^36, at most 2^31 - 1 workgroups, and
+ * workspace_bytes; batch, queries or heads 0 is a no-op; keys == 0 writes o = 0
+ * and lse = -inf.  Nulls (TERN_ERR_NULL; k and v with keys > 0).  Strides not
+ * negative, token strides below 2^22, ldmask >= keys (TERN_ERR_STRIDE).  q, k, v, o
+ * 16-byte aligned with strides that are multiples of 8 (the stride of an axis
+ * of one element is not looked at), lse 4-byte aligned (TERN_ERR_ALIGN).
+ */
+tern_status tern_attention(const tern_heads* q, const tern_heads* k, const tern_heads* v,
+                           const tern_heads* o, const tern_attention_shape* shape,
+                           const uint8_t* mask, int64_t ldmask, float* lse, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tern_attention (backward == 0) or tern_attention_bwd
+ * needs for these sizes (0 for sizes that they refuse). */
+int64_t tern_attention_workspace(const tern_attention_shape* shape, int masked, int backward);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,7 +38,8 @@ EXPORTED = ("tern_quantize", "tern_quantize_pack", "tern_pack", "tern_unpack", "
             "tern_gemm_ex", "tern_pack_transposed", "tern_gemm_dx", "tern_gemm_dx_static",
             "tern_gemm_dw", "tern_quantize_act", "tern_pack_a8", "tern_gemm_a8",
             "tern_rope", "tern_residual_norm", "tern_residual_norm_bwd",
-            "tern_residual_norm_bwd_workspace", "tern_status_string")
+            "tern_residual_norm_bwd_workspace", "tern_attention", "tern_attention_workspace",
+            "tern_status_string")
 
 
 class TernError(RuntimeError):

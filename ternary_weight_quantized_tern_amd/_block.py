@@ -27,12 +27,14 @@ TERN_NORM_NONE = 0
 TERN_NORM_LAYER = 1
 TERN_NORM_RMS = 2
 TERN_RESIDUAL_NORM_MAX_C = 8192
+TERN_ATTENTION_MAX_WIDTH = 128
 
 _i64, _vp, _bytes = ctypes.c_int64, ctypes.c_void_p, ctypes.c_char_p
 # The C structs travel as packed bytes of the same layout.
 _heads_struct = struct.Struct("@4q").pack
 _axes_struct = struct.Struct("@5id2i").pack  # (the layout, then padding to the double's size)
 _norm_struct = struct.Struct("@3q3i2f4x3PqPqPq").pack
+_shape_struct = struct.Struct("@6qf4x").pack
 
 _lib.tern_rope.argtypes = [_bytes, _bytes, ctypes.c_int, _i64, _i64, _i64, _i64, _vp, _i64, _i64,
                            _bytes, ctypes.c_int, _vp]
@@ -44,6 +46,11 @@ _lib.tern_residual_norm_bwd.argtypes = ([_bytes] + [_vp, _i64] * 4 + [_vp] + [_v
 _lib.tern_residual_norm_bwd.restype = ctypes.c_int
 _lib.tern_residual_norm_bwd_workspace.argtypes = [_bytes]
 _lib.tern_residual_norm_bwd_workspace.restype = ctypes.c_int64
+
+_lib.tern_attention.argtypes = [_bytes] * 5 + [_vp, _i64, _vp, _vp, _i64, _vp]
+_lib.tern_attention.restype = ctypes.c_int
+_lib.tern_attention_workspace.argtypes = [_bytes, ctypes.c_int, ctypes.c_int]
+_lib.tern_attention_workspace.restype = ctypes.c_int64
 
 _LAYOUTS = {"interleaved": TERN_ROPE_INTERLEAVED, "halves": TERN_ROPE_HALVES}
 _NORMS = {None: TERN_NORM_NONE, "layer": TERN_NORM_LAYER, "rms": TERN_NORM_RMS}
@@ -227,3 +234,50 @@ def residual_norm_backward(dr_out, dh, r_out: torch.Tensor, y, stats: torch.Tens
         dr.data_ptr(), c, ptr(dy), c, ptr(dgate), ptr(dscale), ptr(dshift), ptr(dpre), ptr(dpost),
         workspace.data_ptr(), need, _stream(stream)))
     return dr, dy, dgate, dscale, dshift, dpre, dpost
+
+
+_BF16 = (torch.bfloat16,)
+
+
+def _attention_shape(q, k, v, scale) -> bytes:
+    b, sq, hq, d = q.shape
+    sk, hkv = k.shape[1], k.shape[2]
+    if k.shape != v.shape or k.shape[0] != b or k.shape[3] != d:
+        raise ValueError(f"shapes must be q [b, s, heads, d], k and v [b, keys, kv_heads, d], got "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    return _shape_struct(b, sq, sk, hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else scale)
+
+
+def _key_mask(mask, b: int, keys: int):
+    """(pointer, pitch) of a [b, keys] mask of truth values or bytes, or None."""
+    if mask is None:
+        return None, 0
+    if not isinstance(mask, torch.Tensor) or not mask.is_cuda or \
+            mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("mask must be a GPU tensor of dtype torch.bool or torch.uint8")
+    if tuple(mask.shape) != (b, keys) or (keys > 1 and mask.stride(1) != 1):
+        raise ValueError(f"mask must be [{b}, {keys}] with consecutive keys")
+    # An empty mask has no address, and masks nothing.
+    return mask.data_ptr() or None, max(mask.stride(0), keys) if b > 1 else keys
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask=None,
+              scale: float | None = None, stream=None):
+    """Attention of ``q`` [b, s, heads, d] to ``k``, ``v`` [b, keys, kv_heads, d] (bf16, any
+    strides with consecutive channels that are multiples of 8; ``kv_heads``
+    divides ``heads``, ``d`` a multiple of 8 up to 128).  ``mask`` [b, keys] (bool
+    or uint8) keeps the keys that are true; a row without a kept key gives 0.
+    ``scale`` defaults to ``1 / sqrt(d)``.  Returns ``(o, lse)``: bf16 [b, s,
+    heads, d] and the fp32 log-sum-exps [b, heads, s] for the backward pass."""
+    qs, ks, vs = _heads(q, "q", _BF16), _heads(k, "k", _BF16), _heads(v, "v", _BF16)
+    b, s, h, d = q.shape
+    shape = _attention_shape(q, k, v, scale)
+    mp, ldmask = _key_mask(mask, b, k.shape[1])
+    o = torch.empty((b, s, h, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
+    need = _lib.tern_attention_workspace(shape, mp is not None, 0)
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _check("tern_attention", _lib.tern_attention(
+        qs, ks, vs, _heads(o, "o", _BF16), shape, mp, ldmask, lse.data_ptr(),
+        workspace.data_ptr() if need else None, need, _stream(stream)))
+    return o, lse

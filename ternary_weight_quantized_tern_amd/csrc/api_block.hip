@@ -42,6 +42,62 @@ tern_status check_vectors(const tern_residual_norm_args* a, bool with_shift) {
   return TERN_OK;
 }
 
+constexpr int64_t kMaxToken = int64_t(1) << 22;  // token strides: a tile's offsets fit 31 bits
+
+tern_status check_attention(const tern_attention_shape* s) {
+  if (s == nullptr) return TERN_ERR_NULL;
+  if (!(s->scale > 0.0f) || !isfinite(s->scale)) return TERN_ERR_ARG;
+  if (s->batch < 0 || s->queries < 0 || s->keys < 0 || s->heads < 0 || s->kv_heads < 0 ||
+      s->width < 8 || s->width > TERN_ATTENTION_MAX_WIDTH || s->width % 8 != 0)
+    return TERN_ERR_SHAPE;
+  if (s->batch > kMaxInt || s->heads > kMaxInt || s->kv_heads > kMaxInt ||
+      s->queries > (int64_t(1) << 30) || s->keys >= (int64_t(1) << 36))
+    return TERN_ERR_SHAPE;
+  if (s->heads > 0) {
+    if (s->kv_heads == 0 || s->heads % s->kv_heads != 0) return TERN_ERR_SHAPE;
+    if (s->batch * s->heads > kMaxInt ||
+        s->queries * (s->heads / s->kv_heads) >= (int64_t(1) << 30))
+      return TERN_ERR_SHAPE;
+    // The smallest tiles: 32 rows, 64 keys.
+    const int64_t rows = (s->queries * (s->heads / s->kv_heads) + 31) / 32;
+    const int64_t most = kMaxInt / (s->batch > 0 ? s->batch * s->kv_heads : 1);
+    if (rows > most || (s->keys + 63) / 64 > most) return TERN_ERR_SHAPE;
+  }
+  return TERN_OK;
+}
+
+// Strides and alignment of a [batch, tokens, heads, width] view of 16-bit elements.
+tern_status check_view(const tern_heads* v, int64_t batch, int64_t tokens, int64_t heads) {
+  if (!strides_ok(v) || (tokens > 1 && v->token >= kMaxToken)) return TERN_ERR_STRIDE;
+  if (!aligned(v->data, 16) || (batch > 1 && v->batch % 8 != 0) ||
+      (tokens > 1 && v->token % 8 != 0) || (heads > 1 && v->head % 8 != 0))
+    return TERN_ERR_ALIGN;
+  return TERN_OK;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The sizes' part of the kernel's parameters (all that the workspace depends on).
+void fill_shape(tern::AttentionParams& p, const tern_attention_shape& s) {
+  p.b = static_cast<int32_t>(s.batch);
+  p.sq = static_cast<int32_t>(s.queries);
+  p.sk = s.keys;
+  p.hkv = static_cast<int32_t>(s.kv_heads);
+  p.group = static_cast<int32_t>(s.heads / s.kv_heads);
+  p.rows = p.sq * p.group;
+  p.d = static_cast<int32_t>(s.width);
+  p.scale = s.scale;
+  p.scale_log2 = s.scale * kLog2e;
+}
+
+// A view's strides as the kernels use them; those of axes of one element are 0.
+void fill_view(const tern_heads* v, int64_t batch, int64_t tokens, int64_t heads, int64_t& sb,
+               int64_t& st, int64_t& sh) {
+  sb = batch > 1 ? v->batch : 0;
+  st = tokens > 1 ? v->token : 0;
+  sh = heads > 1 ? v->head : 0;
+}
+
 inline uintptr_t size_of(tern_dtype t) { return t == TERN_F32 ? 4 : 2; }
 
 }  // namespace
@@ -223,6 +279,56 @@ tern_status tern_residual_norm_bwd(const tern_residual_norm_args* args, const vo
   p.dpost_weight = dpost_weight;
   return from_hip(tern::launch_residual_norm_bwd(p, a.r_dtype == TERN_BF16, workspace,
                                                  static_cast<hipStream_t>(stream)));
+}
+
+int64_t tern_attention_workspace(const tern_attention_shape* shape, int masked, int backward) {
+  if (check_attention(shape) != TERN_OK || shape->batch == 0 || shape->heads == 0) return 0;
+  tern::AttentionParams p = {};
+  fill_shape(p, *shape);
+  // (The plan depends on whether there is a mask, not on the mask.)
+  p.mask = masked ? reinterpret_cast<const uint8_t*>(1) : nullptr;
+  (void)backward;
+  return shape->queries == 0 ? 0 : tern::attention_workspace(p);
+}
+
+tern_status tern_attention(const tern_heads* q, const tern_heads* k, const tern_heads* v,
+                           const tern_heads* o, const tern_attention_shape* shape,
+                           const uint8_t* mask, int64_t ldmask, float* lse, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  const tern_status bad = check_attention(shape);
+  if (bad != TERN_OK) return bad;
+  const tern_attention_shape& s = *shape;
+  if (s.batch == 0 || s.queries == 0 || s.heads == 0) return TERN_OK;
+  tern::AttentionParams p = {};
+  fill_shape(p, s);
+  p.mask = mask;
+  const int64_t need = tern::attention_workspace(p);
+  if (workspace_bytes < need) return TERN_ERR_SHAPE;
+  if (q == nullptr || o == nullptr || q->data == nullptr || o->data == nullptr ||
+      (s.keys > 0 && (k == nullptr || v == nullptr || k->data == nullptr || v->data == nullptr)) ||
+      (need > 0 && workspace == nullptr))
+    return TERN_ERR_NULL;
+  static const tern_heads none = {};
+  if (s.keys == 0) k = v = &none;
+  if (mask != nullptr && ldmask < s.keys) return TERN_ERR_STRIDE;
+  const tern_heads* views[4] = {q, o, k, v};
+  for (int i = 0; i < 4; ++i) {
+    const tern_status st = check_view(views[i], s.batch, i < 2 ? s.queries : s.keys,
+                                      i < 2 ? s.heads : s.kv_heads);
+    if (st != TERN_OK) return st;
+  }
+  if (!aligned(lse, 4) || (need > 0 && !aligned(workspace, 16))) return TERN_ERR_ALIGN;
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.k = static_cast<const uint16_t*>(k->data);
+  p.v = static_cast<const uint16_t*>(v->data);
+  p.o = static_cast<uint16_t*>(o->data);
+  fill_view(q, s.batch, s.queries, s.heads, p.qb, p.qt, p.qh);
+  fill_view(o, s.batch, s.queries, s.heads, p.ob, p.ot, p.oh);
+  fill_view(k, s.batch, s.keys, s.kv_heads, p.kb, p.kt, p.kh);
+  fill_view(v, s.batch, s.keys, s.kv_heads, p.vb, p.vt, p.vh);
+  p.lse = lse;
+  p.ldmask = ldmask;
+  return from_hip(tern::launch_attention(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,454 @@
+// Attention to keys and values of another length, forward:
+//   S = scale q k^T over the kept keys, P = softmax(S), o = P v, lse = log sum exp S.
+//
+// One pass over the keys with the running maximum m and sum l of each row.  The
+// query rows of all heads that share a key-value head are one block of rows
+// (head by head), so shared keys are read once for the group and few queries of
+// many heads fill a tile.
+//
+// Both products put the rows in the lanes' columns: S^T = K q^T gives lane
+// (i, h) 16 keys of row i, so a row's maximum and sum are in-lane plus one
+// exchange between the halves of the wave, the running values are one register, and
+// exp(S^T) is already the B operand of O^T = V^T P^T (attention_common.h).
+// K is read from LDS by rows, V by transposing reads; q stays in registers.
+//
+// Two forms:
+//  * many rows: four waves of 32 rows each share tiles of 64 keys.  Two
+//    workgroups fit on a CU (two tiles of K and V in LDS each, under 256
+//    registers), so the softmax of one wave runs beside the products of another.
+//  * few rows (at most 64): the four waves take 32 keys each of tiles of 128
+//    for the same 32 rows and are joined through LDS at the end: a stream of keys.
+// With too few workgroups for the chip the keys are split among several, whose
+// normalised parts (fp32) and log-sum-exps a second kernel joins.
+//
+// The maximum is only raised when a row's new one exceeds it by more than 8 in
+// log2 (so exp2 stays below 256 and the sum exact to fp32): after the first
+// tiles the accumulators are hardly ever rescaled.  P is rounded to bf16 for
+// the product with v (the type of every operand of the matrix cores here); S,
+// the maximum, the sum and the accumulators are fp32.
+// Rows of masked keys arrive in LDS as zeros, so what memory holds there (a NaN in
+// padding) does not count; tiles without a kept key are skipped.
+#include "attention_common.h"
+
+namespace tern {
+namespace {
+
+[[maybe_unused]] constexpr float kLn2 = 0.6931471805599453f;
+[[maybe_unused]] constexpr float kRaise = 8.0f;
+
+template <int CPR, int RW, int KW, bool MASK>
+__global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kernel(
+    AttentionParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = RW * KW, kSub = KW == 1 ? 2 : 1, BK = 32 * KW * kSub;
+  constexpr int DS = CPR / 2, DT = (CPR + 3) / 4;
+  constexpr int kWords = BK / 64;
+  constexpr uint32_t kBytes = tile_bytes<CPR>(BK);
+  __shared__ __attribute__((aligned(1024))) uint8_t k0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t k1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t v0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t v1[kBytes];
+  __shared__ unsigned long long words[MASK ? kMaskWords : 1];
+  __shared__ float2 joined[KW > 1 ? KW : 1][32];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, kw = wave / RW;
+  const int i = lane & 31, h = lane >> 5;
+
+  // Row block fastest, then split, kv head, sample.
+  uint32_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int block = at % p.row_blocks;
+  at /= p.row_blocks;
+  const int split = at % p.splits;
+  const uint32_t bh = at / p.splits;
+  const int hk = bh % p.hkv, b = bh / p.hkv;
+
+  const int t_first = split * p.tiles_per_split;
+  const int t_end = t_first + p.tiles_per_split < p.tiles ? t_first + p.tiles_per_split : p.tiles;
+  if (MASK) {
+    mask_words(words, p.mask + b * p.ldmask, static_cast<int64_t>(t_first) * BK, p.sk,
+               (t_end - t_first) * kWords, wave, NW, lane);
+    __syncthreads();
+  }
+
+  // The rows of this lane's column, as the B operand of S^T.
+  const int row = (block * RW + rw) * 32 + i;
+  const PackedRow pr = packed_row(row, p.rows, p.sq);
+  bf16x8_t qf[DS];
+  {
+    const uint16_t* q = p.q + b * p.qb + static_cast<int64_t>(pr.token) * p.qt +
+                        static_cast<int64_t>(hk * p.group + pr.head) * p.qh;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const int c = 16 * s + 8 * h;
+      qf[s] = bf16x8_t{};
+      if (pr.live && c < p.d) qf[s] = *reinterpret_cast<const bf16x8_t*>(q + c);
+    }
+  }
+
+  const uint16_t* kbase = p.k + b * p.kb + hk * p.kh;
+  const uint16_t* vbase = p.v + b * p.vb + hk * p.vh;
+  TileCopy<CPR, BK, NW> kcopy, vcopy;
+  kcopy.plan(wave, lane, p.kt, p.d);
+  vcopy.plan(wave, lane, p.vt, p.d);
+
+  uint32_t koff[DS], voffa[DT], voffb[DT];
+  const uint32_t first_key = kw * (32 * kSub);  // of this wave, in a tile
+#pragma unroll
+  for (int s = 0; s < DS; ++s) koff[s] = tile_offset<CPR>(first_key + i, 2 * s + h);
+#pragma unroll
+  for (int t = 0; t < DT; ++t) {
+    transposed_offsets<CPR>(lane, t, voffa[t], voffb[t]);
+    voffa[t] += first_key * (CPR * 16u);
+    voffb[t] += first_key * (CPR * 16u);
+  }
+
+  auto word_of = [&](int t, int w) -> unsigned long long {
+    if (MASK) return uniform64(words[(t - t_first) * kWords + w]);
+    return tail_word(static_cast<int64_t>(t) * BK + 64 * w, p.sk);
+  };
+  auto next_tile = [&](int t) {
+    if (MASK)
+      while (t < t_end) {
+        unsigned long long any = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) any |= word_of(t, w);
+        if (any) break;
+        ++t;
+      }
+    return t;
+  };
+  auto issue = [&](int t, uint8_t* kl, uint8_t* vl) {
+    unsigned long long w[kWords];
+    bool all = true;
+#pragma unroll
+    for (int x = 0; x < kWords; ++x) {
+      w[x] = word_of(t, x);
+      all = all && w[x] == ~0ull;
+    }
+    auto keep = [&](uint32_t r) {
+      const unsigned long long bits = kWords == 2 && r >= 64 ? w[kWords - 1] : w[0];
+      return ((bits >> (r & 63u)) & 1ull) != 0;
+    };
+    kcopy.issue(kbase + static_cast<int64_t>(t) * BK * p.kt, kl, wave, lane, all, keep);
+    vcopy.issue(vbase + static_cast<int64_t>(t) * BK * p.vt, vl, wave, lane, all, keep);
+  };
+
+  f32x16_t o[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) o[t] = f32x16_t{};
+  float m = -INFINITY, l = 0.0f;
+
+  auto compute = [&](int t, const uint8_t* kl, const uint8_t* vl) {
+    f32x16_t s[kSub];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) s[u] = f32x16_t{};
+#pragma unroll
+    for (int c = 0; c < DS; ++c)
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+        s[u] = mfma32(read_rows(kl, koff[c] + u * (32 * CPR * 16u)), qf[c], s[u]);
+
+    // Masked keys: S = -inf.
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      const int key = first_key + 32 * u;
+      const uint32_t part = static_cast<uint32_t>(word_of(t, key >> 6) >> (key & 63));
+      if (part != 0xFFFFFFFFu) {
+        const uint32_t mine = part >> (4 * h);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          s[u][e] = (mine >> ((e & 3) + 8 * (e >> 2))) & 1u ? s[u][e] : -INFINITY;
+      }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
+    float lo, hi;
+    halves(top, lo, hi);
+    top = fmaxf(lo, hi);
+    if (__ballot((top - m) * p.scale_log2 > kRaise)) {
+      const float to = fmaxf(m, top);
+      const float a = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - to) * p.scale_log2);
+      m = to;
+      l *= a;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] *= a;
+    }
+    const float shift = m == -INFINITY ? 0.0f : m * p.scale_log2;
+    bf16x8_t pf[2 * kSub];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], p.scale_log2, -shift));
+        l += x[e];
+      }
+      pf[2 * u] = to_operand(x);
+      pf[2 * u + 1] = to_operand(x + 8);
+    }
+#pragma unroll
+    for (int c = 0; c < 2 * kSub; ++c)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        o[d] = mfma32(read_transposed(vl, voffa[d] + c * (16 * CPR * 16u),
+                                      voffb[d] + c * (16 * CPR * 16u)),
+                      pf[c], o[d]);
+  };
+
+  // Two tiles in LDS: while one is used the next is on its way.
+  int t = next_tile(t_first);
+  if (t < t_end) issue(t, k0, v0);
+  while (t < t_end) {
+    wait_vmem();
+    tile_barrier();
+    int n = next_tile(t + 1);
+    if (n < t_end) issue(n, k1, v1);
+    compute(t, k0, v0);
+    t = n;
+    if (t >= t_end) break;
+    wait_vmem();
+    tile_barrier();
+    n = next_tile(t + 1);
+    if (n < t_end) issue(n, k0, v0);
+    compute(t, k1, v1);
+    t = n;
+  }
+
+  {
+    float lo, hi;
+    halves(l, lo, hi);
+    l = lo + hi;
+  }
+  if constexpr (KW == 1) {
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float lse2 = l > 0.0f ? __builtin_fmaf(m, p.scale_log2, __builtin_amdgcn_logf(l)) : -INFINITY;
+    if (p.splits > 1) {
+      const int64_t r = (static_cast<int64_t>(split) * p.b * p.hkv + bh) * p.rows + row;
+      if (pr.live) {
+        if (h == 0) p.part_lse[r] = lse2;
+        float* out = p.part_o + r * p.d;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int c = 32 * d + 8 * g + 4 * h;
+            if (c < p.d)
+              *reinterpret_cast<f32x4_t*>(out + c) =
+                  f32x4_t{o[d][4 * g] * inv, o[d][4 * g + 1] * inv, o[d][4 * g + 2] * inv,
+                          o[d][4 * g + 3] * inv};
+          }
+      }
+    } else {
+      const int head = hk * p.group + pr.head;
+      if (pr.live && h == 0 && p.lse != nullptr)
+        p.lse[(static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + pr.token] = lse2 * kLn2;
+      uint16_t* out = p.o + b * p.ob + static_cast<int64_t>(pr.token) * p.ot +
+                      static_cast<int64_t>(head) * p.oh;
+      // Lane (i, h) holds channels 8 g + 4 h .. + 3; the halves trade so that
+      // each has eight consecutive ones.
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int e = 4 * g + 2 * x;  // x = 0, 1: group g; x = 2, 3: group g + 1
+            const bf16x2_t two = {static_cast<__bf16>(o[d][e] * inv),
+                                  static_cast<__bf16>(o[d][e + 1] * inv)};
+            w[x] = __builtin_bit_cast(uint32_t, two);
+          }
+          const auto a0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+          const auto a1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+          const int c = 32 * d + 8 * g + 8 * h;
+          const u32x4_t v = {a0[0], a1[0], a0[1], a1[1]};
+          if (pr.live && c < p.d) *reinterpret_cast<u32x4_t*>(out + c) = v;
+        }
+    }
+  } else {
+    // Join the waves' parts of the same rows.
+    if (h == 0) joined[kw][i] = make_float2(m, l);
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) top = fmaxf(top, joined[w][i].x);
+    const float mine = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - top) * p.scale_log2);
+    float total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const float2 j = joined[w][i];
+      if (j.y > 0.0f) total += j.y * __builtin_amdgcn_exp2f((j.x - top) * p.scale_log2);
+    }
+    const float inv = total > 0.0f ? mine / total : 0.0f;
+    // [32 rows][32 DT channels] of each wave, in the tiles' buffers.
+    float* parts[4] = {reinterpret_cast<float*>(k0), reinterpret_cast<float*>(k1),
+                       reinterpret_cast<float*>(v0), reinterpret_cast<float*>(v1)};
+    static_assert(KW == 4 && kBytes >= 32u * 32 * DT * 4, "a wave's part fits a buffer");
+    float* own = kw == 0 ? parts[0] : kw == 1 ? parts[1] : kw == 2 ? parts[2] : parts[3];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        own[i * (32 * DT) + 32 * d + (e & 3) + 8 * (e >> 2) + 4 * h] = o[d][e] * inv;
+    __syncthreads();
+    const float lse2 =
+        total > 0.0f ? __builtin_fmaf(top, p.scale_log2, __builtin_amdgcn_logf(total)) : -INFINITY;
+    const int head = hk * p.group + pr.head;
+    const int64_t part_row = (static_cast<int64_t>(split) * p.b * p.hkv + bh) * p.rows;
+    if (wave == 0 && h == 0 && pr.live) {
+      if (p.splits > 1)
+        p.part_lse[part_row + row] = lse2;
+      else if (p.lse != nullptr)
+        p.lse[(static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + pr.token] = lse2 * kLn2;
+    }
+    // Eight channels a thread.
+    for (int x = threadIdx.x; x < 32 * CPR; x += 64 * NW) {
+      const int r = x / CPR, c = (x % CPR) * 8;
+      const PackedRow to = packed_row(block * 32 + r, p.rows, p.sq);
+      if (!to.live || c >= p.d) continue;
+      float sum[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int off = r * (32 * DT) + c + e;
+        sum[e] = (parts[0][off] + parts[1][off]) + (parts[2][off] + parts[3][off]);
+      }
+      if (p.splits > 1) {
+        float* out = p.part_o + (part_row + block * 32 + r) * p.d + c;
+        *reinterpret_cast<f32x4_t*>(out) = f32x4_t{sum[0], sum[1], sum[2], sum[3]};
+        *reinterpret_cast<f32x4_t*>(out + 4) = f32x4_t{sum[4], sum[5], sum[6], sum[7]};
+      } else {
+        uint16_t* out = p.o + b * p.ob + static_cast<int64_t>(to.token) * p.ot +
+                        static_cast<int64_t>(hk * p.group + to.head) * p.oh + c;
+        *reinterpret_cast<bf16x8_t*>(out) = to_operand(sum);
+      }
+    }
+  }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// The parts of a row, weighted by their shares of the sum: eight channels a thread.
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) {
+  const int chunks = p.d / 8;
+  const int64_t rows = static_cast<int64_t>(p.b) * p.hkv * p.rows;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (x >= rows * chunks) return;
+  const int64_t r = x / chunks;
+  const int c = static_cast<int>(x - r * chunks) * 8;
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * rows + r]);
+  float total = 0.0f, sum[8] = {};
+  if (top > -INFINITY) {
+    for (int s = 0; s < p.splits; ++s) {
+      const float w = __builtin_amdgcn_exp2f(p.part_lse[s * rows + r] - top);
+      const float* in = p.part_o + (s * rows + r) * p.d + c;
+      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(in);
+      const f32x4_t q = *reinterpret_cast<const f32x4_t*>(in + 4);
+      total += w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum[e] = __builtin_fmaf(w, a[e], sum[e]);
+        sum[4 + e] = __builtin_fmaf(w, q[e], sum[4 + e]);
+      }
+    }
+    const float inv = 1.0f / total;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] *= inv;
+  }
+  const int64_t bh = r / p.rows;
+  const int row = static_cast<int>(r - bh * p.rows);
+  const int b = static_cast<int>(bh / p.hkv), hk = static_cast<int>(bh - static_cast<int64_t>(b) * p.hkv);
+  const PackedRow to = packed_row(row, p.rows, p.sq);
+  const int head = hk * p.group + to.head;
+  *reinterpret_cast<bf16x8_t*>(p.o + b * p.ob + static_cast<int64_t>(to.token) * p.ot +
+                               static_cast<int64_t>(head) * p.oh + c) = to_operand(sum);
+  if (c == 0 && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + to.token] =
+        top > -INFINITY ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+}
+
+constexpr int kFewRows = 64;
+
+struct Plan {
+  bool few;
+  int tiles, tiles_per_split, splits, row_blocks;
+  int64_t part_bytes;
+};
+
+// Few rows: split until there is a workgroup for each CU (one fits on it); many
+// rows: two for each.  A part has at least two tiles (few) or four, and with a
+// mask at most what fits its words.
+Plan plan(const AttentionParams& p) {
+  Plan r;
+  r.few = p.rows <= kFewRows;
+  const int bk = r.few ? 128 : 64, least = r.few ? 2 : 4;
+  const int64_t wanted = r.few ? 256 : 512;
+  r.row_blocks = (p.rows + (r.few ? 31 : 127)) / (r.few ? 32 : 128);
+  r.tiles = static_cast<int>((p.sk + bk - 1) / bk);
+  const int64_t base = static_cast<int64_t>(p.b) * p.hkv * r.row_blocks;
+  int64_t splits = wanted / base;
+  if (splits > r.tiles / least) splits = r.tiles / least;
+  if (splits < 1) splits = 1;
+  const int most = p.mask ? kMaskWords * 64 / bk : 1 << 30;
+  const int64_t forced = (static_cast<int64_t>(r.tiles) + most - 1) / most;
+  if (splits < forced) splits = forced;
+  r.tiles_per_split = static_cast<int>((r.tiles + splits - 1) / splits);
+  if (r.tiles_per_split < 1) r.tiles_per_split = 1;
+  r.splits = (r.tiles + r.tiles_per_split - 1) / r.tiles_per_split;
+  if (r.splits < 1) r.splits = 1;
+  const int64_t rows = static_cast<int64_t>(p.b) * p.hkv * p.rows;
+  r.part_bytes = r.splits > 1 ? r.splits * rows * (p.d + 1) * 4 : 0;
+  return r;
+}
+
+template <int CPR>
+hipError_t launch(const AttentionParams& p, bool few, int64_t grid, hipStream_t stream) {
+  const dim3 g(static_cast<unsigned>(grid)), b(256);
+  if (few) {
+    if (p.mask)
+      hipLaunchKernelGGL((attention_kernel<CPR, 1, 4, true>), g, b, 0, stream, p);
+    else
+      hipLaunchKernelGGL((attention_kernel<CPR, 1, 4, false>), g, b, 0, stream, p);
+  } else {
+    if (p.mask)
+      hipLaunchKernelGGL((attention_kernel<CPR, 4, 1, true>), g, b, 0, stream, p);
+    else
+      hipLaunchKernelGGL((attention_kernel<CPR, 4, 1, false>), g, b, 0, stream, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t attention_workspace(const AttentionParams& p) { return plan(p).part_bytes; }
+
+hipError_t launch_attention(AttentionParams& p, void* workspace, hipStream_t stream) {
+  const Plan r = plan(p);
+  p.tiles = r.tiles;
+  p.tiles_per_split = r.tiles_per_split;
+  p.splits = r.splits;
+  p.row_blocks = r.row_blocks;
+  const int64_t rows = static_cast<int64_t>(p.b) * p.hkv * p.rows;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + r.splits * rows * p.d;
+  const int64_t grid = static_cast<int64_t>(p.b) * p.hkv * r.row_blocks * r.splits;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const hipError_t e = p.d <= 32   ? launch<4>(p, r.few, grid, stream)
+                       : p.d <= 64 ? launch<8>(p, r.few, grid, stream)
+                       : p.d <= 80 ? launch<10>(p, r.few, grid, stream)
+                       : p.d <= 96 ? launch<12>(p, r.few, grid, stream)
+                                   : launch<16>(p, r.few, grid, stream);
+  if (e != hipSuccess || r.splits == 1) return e;
+  const int64_t threads = rows * (p.d / 8);
+  hipLaunchKernelGGL(attention_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)),
+                     dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace tern

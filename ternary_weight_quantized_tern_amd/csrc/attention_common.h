@@ -1,0 +1,193 @@
+// Device helpers shared by the attention kernels: the layout of a tile of rows
+// in LDS, its staging, the operands read from it, and the key mask.  Internal
+// to libternary.
+//
+// Products are v_mfma_f32_32x32x16_bf16 through the compiler's builtin: lane l
+// (i = l % 32, h = l / 32) gives row i of A and column i of B, values k = 8 h ..
+// 8 h + 7, and receives column i of D, rows (e % 4) + 8 (e / 4) + 4 h for e =
+// 0 .. 15.  The contraction may take its 16 values in any order as long as A
+// and B agree, so the rows that a lane receives of one product,
+// {4 h .. 4 h + 3, 8 + 4 h ..}, serve as its share of the contraction of the next: the
+// probabilities go from one product to the other without leaving their lane.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_common.h"
+#include "internal.h"
+#include "wave.h"
+
+namespace tern {
+
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
+typedef __attribute__((ext_vector_type(4))) short i16x4_t;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+
+// Rows of a tile lie in LDS as CPR 16-byte chunks (CPR = 4, 8, 10, 12, 16 for
+// head widths up to 32, 64, 80, 96, 128), the chunks of a row permuted by an
+// exclusive or with tile_swizzle(row).  It is chosen so that the two kinds of
+// read spread over all 64 banks (256 bytes): 16 consecutive rows at one chunk
+// (operands by rows), and four consecutive rows at four consecutive chunks
+// (transposing reads; at CPR = 10 those meet in two banks of a row).
+template <int CPR>
+__host__ __device__ constexpr uint32_t tile_swizzle(uint32_t row) {
+  return CPR == 16   ? ((row & 3u) << 2) | ((row >> 2) & 3u)
+         : CPR == 8  ? ((row & 2u) << 1) | ((row >> 2) & 3u)
+         : CPR == 10 ? (row >> 3) & 1u
+                     : (row >> 2) & 3u;
+}
+
+template <int CPR>
+__device__ inline uint32_t tile_offset(uint32_t row, uint32_t chunk) {
+  return row * (CPR * 16u) + ((chunk ^ tile_swizzle<CPR>(row)) << 4);
+}
+
+// A transposing read of a 32-channel group may run past a row of 10 chunks (its
+// products are not stored); the last row's then still lies in the buffer.
+template <int CPR>
+constexpr uint32_t tile_bytes(int rows) {
+  return rows * CPR * 16u + (CPR == 10 ? 64u : 0u);
+}
+
+__device__ inline void wait_vmem() {
+  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // vmcnt(0) only
+}
+
+// Barrier that orders LDS accesses without __syncthreads()' fence, which would also
+// wait for the copies in flight.
+__device__ inline void tile_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Copies of a tile's rows into LDS by NW waves, 1 KiB an instruction: which
+// row and chunk each lane brings, as a byte offset from the tile's first row.
+template <int CPR, int ROWS, int NW>
+struct TileCopy {
+  static constexpr int kInstr = ROWS * CPR / 64;       // of the tile
+  static constexpr int kOwn = (kInstr + NW - 1) / NW;  // at most, of one wave
+  static constexpr uint32_t kNone = 0x80000000u;       // outside every range: reads 0
+
+  uint32_t offset[kOwn];
+
+  __device__ static uint32_t row(int q, int wave, int lane) {
+    return static_cast<uint32_t>((wave + NW * q) * 64 + lane) / CPR;
+  }
+  __device__ void plan(int wave, int lane, int64_t stride, int d) {
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) {
+      const uint32_t slot = static_cast<uint32_t>((wave + NW * q) * 64 + lane);
+      const uint32_t r = slot / CPR, c = (slot % CPR) ^ tile_swizzle<CPR>(r);
+      offset[q] = static_cast<int>(8 * c) < d
+                      ? r * static_cast<uint32_t>(stride) * 2u + 16u * c
+                      : kNone;
+    }
+  }
+  // keep(row): whether the row is read (else it arrives as zeros).
+  template <typename Keep>
+  __device__ void issue(const uint16_t* base, uint8_t* lds, int wave, int lane, bool all,
+                        Keep keep) const {
+    const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(base, 0x7FFFFFFFu);
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) {
+      if (kInstr % NW != 0 && wave + NW * q >= kInstr) break;
+      uint32_t off = offset[q];
+      if (!all && !keep(row(q, wave, lane))) off = kNone;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (lds_void_t*)(lds + 1024u * static_cast<uint32_t>(wave + NW * q)), 16, off, 0, 0,
+          0);
+    }
+  }
+};
+
+// An operand by rows: lane (i, h) of row row0 + i, channels 16 step + 8 h .. + 7.
+__device__ inline bf16x8_t read_rows(const uint8_t* lds, uint32_t offset) {
+  return *reinterpret_cast<const bf16x8_t*>(lds + offset);
+}
+
+// A transposed operand: lane (i, h) gets channel c0 + i of rows r .. r + 3 (first
+// read, at `a`) and of rows r + 8 .. r + 11 (second, at `b`), r = 4 h.  Within each
+// 16 lanes, lane 4 j + k reads four channels of row j and lane l receives
+// channel l of the four rows.
+__device__ inline bf16x8_t read_transposed(const uint8_t* lds, uint32_t a, uint32_t b) {
+  typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + a));
+  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + b));
+  const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+  const u32x4_t v = {l2.x, l2.y, h2.x, h2.y};
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// Offsets of a lane's transposing reads of 32-channel group dt, rows 0 .. 15 of a
+// tile (16 rows on: 16 CPR * 16 bytes more; the swizzle repeats every 16 rows).
+template <int CPR>
+__device__ inline void transposed_offsets(int lane, int dt, uint32_t& a, uint32_t& b) {
+  const uint32_t h = lane >> 5, g = (lane >> 4) & 1, j = (lane >> 2) & 3, k = lane & 3;
+  const uint32_t chunk = 4u * dt + 2u * g + (k >> 1), sub = (k & 1u) * 8u;
+  a = tile_offset<CPR>(4u * h + j, chunk) + sub;
+  b = tile_offset<CPR>(4u * h + j + 8u, chunk) + sub;
+}
+
+__device__ inline f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Eight fp32 values as an operand (round to nearest even).
+__device__ inline bf16x8_t to_operand(const float* f) {
+  bf16x8_t v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = static_cast<__bf16>(f[e]);
+  return v;
+}
+
+// A workgroup's place, renumbered so that each of the eight XCDs (workgroups
+// are dealt to them in turn) gets a contiguous run: neighbours share keys in
+// one L2.
+__device__ inline uint32_t xcd_order(uint32_t bid, uint32_t grid) {
+  const uint32_t xcd = bid & 7u, per = grid >> 3, rem = grid & 7u;
+  return xcd * per + (xcd < rem ? xcd : rem) + (bid >> 3);
+}
+
+// The row of lane i of a packed row block: rows of the heads that share a
+// key-value head, head by head.
+struct PackedRow {
+  int head, token;
+  bool live;
+};
+__device__ inline PackedRow packed_row(int row, int rows, int sq) {
+  PackedRow r;
+  r.live = row < rows;
+  const uint32_t at = r.live ? row : 0;
+  r.head = at / static_cast<uint32_t>(sq);
+  r.token = at - r.head * sq;
+  return r;
+}
+
+constexpr int kMaskWords = 1024;  // 64 keys each: the most that one workgroup walks over
+
+// Bits of `words` x 64 keys from key0 on, one word per 64 keys, into LDS.
+__device__ inline void mask_words(unsigned long long* words, const uint8_t* mask, int64_t key0,
+                                  int64_t keys, int count, int wave, int waves, int lane) {
+  for (int w = wave; w < count; w += waves) {
+    const int64_t key = key0 + 64 * w + lane;
+    const bool keep = key < keys && mask[key] != 0;
+    const unsigned long long bits = __ballot(keep);
+    if (lane == 0) words[w] = bits;
+  }
+}
+
+__device__ inline unsigned long long uniform64(unsigned long long v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return (static_cast<unsigned long long>(hi) << 32) | lo;
+}
+
+// Bits of the keys below `keys` among 64 from key0 on.
+__device__ inline unsigned long long tail_word(int64_t key0, int64_t keys) {
+  const int64_t n = keys - key0;
+  return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+}
+
+}  // namespace tern

@@ -148,4 +148,24 @@ int64_t residual_norm_bwd_workspace(int64_t m, int64_t c, int64_t tokens);
 hipError_t launch_residual_norm_bwd(ResidualNormBwdParams& params, bool r_is_bf16, void* workspace,
                                     hipStream_t stream);
 
+// Attention to keys and values of another length.  Row strides (elements) of
+// q, k, v, o: sample, token, head.  rows = group * sq query rows share a kv head.
+struct AttentionParams {
+  const uint16_t *q, *k, *v;
+  int64_t qb, qt, qh, kb, kt, kh, vb, vt, vh;
+  uint16_t* o;
+  int64_t ob, ot, oh;
+  float* lse;  // [b, hkv * group, sq] or nullptr
+  const uint8_t* mask;
+  int64_t ldmask;
+  int32_t b, sq, hkv, group, d, rows;
+  int64_t sk;
+  float scale, scale_log2;
+
+  int32_t tiles, tiles_per_split, splits, row_blocks;
+  float *part_o, *part_lse;  // in the workspace
+};
+int64_t attention_workspace(const AttentionParams& params);
+hipError_t launch_attention(AttentionParams& params, void* workspace, hipStream_t stream);
+
 }  // namespace tern

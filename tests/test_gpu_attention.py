@@ -1,0 +1,236 @@
+"""Attention to keys of another length (tern_attention and its gradients)
+against the formulas in 64 bits.
+
+Tolerances, fixed by the arithmetic.  With P the probabilities in 64 bits and u
+= 2^-8 (half the spacing of bf16, 2^-7, relative): the kernel rounds each unnormalised
+probability to bf16 (relative u each) and the result once, everything else is fp32, so
+
+  |o - o_ref| <= u sum_s P_s |v_s| + u |o_ref| + 2^-16 sum_s P_s |v_s|;
+
+the logits are fp32 sums of up to 128 exact products: their error e_S <= 2^-17 scale
+|q| . |k| moves every P by that, relative.  lse is off by e_S and a few units of
+fp32.  Backward, P and dS are rounded once as operands, so each gradient is
+within u of the sum of its terms' sizes plus u of itself, and the fp32 steps
+add e_S-sized terms; delta = <do, o> is taken of the stored o in both.
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from parity import DEV, log
+
+pytestmark = pytest.mark.gpu
+tern = pytest.importorskip("ternary_weight_quantized_tern_amd")
+
+U = 2.0 ** -8
+
+
+def make(b, sq, sk, hq, hkv, d, mask, seed, spread=1.4, offset=0.0):
+    g = torch.Generator().manual_seed(seed)
+
+    def t(s, h):
+        return (spread * torch.randn(b, s, h, d, generator=g) + offset).to(torch.bfloat16).to(DEV)
+
+    q, k, v = t(sq, hq), t(sk, hkv), t(sk, hkv)
+    m = None
+    if mask == "random":
+        m = torch.rand(b, sk, generator=g) < 0.6
+    elif mask == "prefix":
+        m = torch.arange(sk)[None] < torch.randint(0, sk + 1, (b, 1), generator=g)
+    elif mask == "suffix":  # left padding, whole tiles of it
+        m = torch.arange(sk)[None] >= torch.randint(0, sk + 1, (b, 1), generator=g)
+    elif mask == "none_kept":
+        m = torch.zeros(b, sk, dtype=torch.bool)
+    elif mask == "one":
+        m = torch.zeros(b, sk, dtype=torch.bool)
+        m[torch.arange(b), torch.randint(0, sk, (b,), generator=g)] = True
+    return q, k, v, None if m is None else m.to(DEV)
+
+
+def group(x, hkv):
+    """[b, s, h, d] -> [b, hkv, h / hkv, s, d] in 64 bits."""
+    b, s, h, d = x.shape
+    return x.double().view(b, s, hkv, h // hkv, d).permute(0, 2, 3, 1, 4)
+
+
+def ungroup(x):
+    b, hkv, g, s, d = x.shape
+    return x.permute(0, 3, 1, 2, 4).reshape(b, s, hkv * g, d)
+
+
+def logits(q, k, mask, scale):
+    """S (masked: -inf) and the bound of its error."""
+    hkv = k.shape[2]
+    qd, kd = group(q, hkv), group(k, hkv)
+    s = scale * (qd @ kd.transpose(-1, -2))
+    err = 2.0 ** -17 * scale * (qd.abs() @ kd.abs().transpose(-1, -2))
+    if mask is not None:
+        s = s.masked_fill(~mask[:, None, None, None, :], -math.inf)
+        err = err.masked_fill(~mask[:, None, None, None, :], 0.0)
+    return s, err
+
+
+def probabilities(s):
+    if s.shape[-1] == 0:
+        return s
+    return torch.where(torch.isneginf(s.amax(-1, keepdim=True)), 0.0, torch.softmax(s, -1)).nan_to_num()
+
+
+def within(got, ref, bound, what):
+    off = (got.double() - ref).abs()
+    assert bool(torch.isfinite(got).all()), (what, "not finite")
+    assert bool((off <= bound + 1e-30).all()), (what, float((off - bound).max()), float(off.max()))
+
+
+def check_forward(q, k, v, mask, scale, o, lse, what):
+    hkv = k.shape[2]
+    scale = 1 / math.sqrt(q.shape[3]) if scale is None else scale
+    s, err = logits(q, k, mask, scale)
+    p = probabilities(s)
+    vd = group(v, hkv)
+    ref = ungroup(p @ vd)
+    e = err.amax(-1, keepdim=True) if s.shape[-1] else torch.zeros_like(p[..., :1])
+    size = ungroup((p * (U + 2.0 ** -16 + 2 * e)) @ vd.abs()) if s.shape[-1] else ref
+    within(o, ref, size + U * ref.abs(), what + ": o")
+    b, sq, hq, _ = q.shape
+    ref_lse = torch.logsumexp(s, -1).reshape(b, hq, sq) if s.shape[-1] else torch.full(
+        (b, hq, sq), -math.inf, dtype=torch.float64, device=DEV)
+    assert bool((torch.isneginf(lse) == torch.isneginf(ref_lse)).all()), what
+    fine = ~torch.isneginf(ref_lse)
+    bound = e.reshape(b, hq, sq) + 2.0 ** -20 * (1 + ref_lse.abs())
+    assert bool(((lse.double() - ref_lse).abs()[fine] <= bound[fine]).all()), what + ": lse"
+
+
+FORWARD = [
+    # b, sq, sk, hq, hkv, d, mask
+    (1, 1, 1, 1, 1, 8, None),
+    (2, 1, 300, 8, 2, 64, None),           # one token, shared heads
+    (3, 1, 4096 + 5, 4, 4, 128, "random"),  # one token, the keys split among workgroups
+    (1, 16, 1000, 6, 2, 72, "prefix"),     # few rows
+    (2, 64, 129, 2, 2, 128, "suffix"),
+    (2, 65, 64, 2, 1, 128, None),          # one row past the few-row form with one head
+    (2, 200, 77, 16, 16, 72, "prefix"),    # captions
+    (1, 129, 63, 3, 3, 40, "random"),
+    (2, 130, 65, 4, 2, 32, "random"),
+    (1, 300, 513, 2, 2, 96, None),
+    (2, 257, 320, 4, 4, 80, "suffix"),
+    (1, 100, 2000, 2, 1, 128, None),       # many rows, keys split
+    (3, 50, 128, 6, 2, 24, "one"),
+    (2, 70, 90, 2, 2, 64, "none_kept"),
+    (2, 5, 90, 2, 2, 16, "none_kept"),
+    (1, 256, 256, 8, 8, 128, None),
+]
+
+
+@pytest.mark.parametrize("b,sq,sk,hq,hkv,d,mask", FORWARD)
+def test_forward_matches_the_formula(b, sq, sk, hq, hkv, d, mask):
+    log(f"attention b={b} sq={sq} sk={sk} hq={hq} hkv={hkv} d={d} mask={mask}")
+    q, k, v, m = make(b, sq, sk, hq, hkv, d, mask, seed=sq + 3 * sk + d)
+    o, lse = tern.attention(q, k, v, mask=m)
+    torch.cuda.synchronize()
+    check_forward(q, k, v, m, None, o, lse, f"{b} {sq} {sk} {hq} {hkv} {d} {mask}")
+    o2, lse2 = tern.attention(q, k, v, mask=m)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_forward_large_logits_and_late_maximum():
+    # The largest logit comes last and far above the rest: the running maximum
+    # is raised in the last tile; and logits of several hundred stay finite.
+    log("attention large logits")
+    q, k, v, _ = make(1, 150, 400, 2, 2, 64, None, seed=7, spread=1.0)
+    k[:, 380] = (8 * q[:, 3]).to(torch.bfloat16)
+    k[:, 0] = (3 * q[:, 5]).to(torch.bfloat16)
+    o, lse = tern.attention(q, k, v, scale=1.0)
+    check_forward(q, k, v, None, 1.0, o, lse, "large logits")
+    # a small step between tiles, below the threshold that raises the maximum
+    q, k, v, _ = make(1, 150, 400, 2, 2, 64, None, seed=8, spread=0.3)
+    o, lse = tern.attention(q, k, v, scale=0.5)
+    check_forward(q, k, v, None, 0.5, o, lse, "small logits")
+
+
+@pytest.mark.parametrize("sq", [3, 140])
+def test_forward_ignores_what_masked_keys_hold(sq):
+    log(f"attention masked NaN sq={sq}")
+    q, k, v, m = make(2, sq, 333, 4, 2, 72, "random", seed=11)
+    clean, clean_lse = tern.attention(q, k, v, mask=m)
+    for bad in (float("nan"), float("inf"), torch.finfo(torch.bfloat16).min):
+        kb = torch.where(m[:, :, None, None], k, torch.full_like(k, bad))
+        vb = torch.where(m[:, :, None, None], v, torch.full_like(v, bad))
+        o, lse = tern.attention(q, kb, vb, mask=m)
+        assert torch.equal(o, clean) and torch.equal(lse, clean_lse), bad
+
+
+@pytest.mark.parametrize("sq", [2, 90])
+def test_forward_strides_layouts_and_broadcasts(sq):
+    log(f"attention strides sq={sq}")
+    g = torch.Generator().manual_seed(3)
+    b, sk, h, d = 2, 100, 3, 64
+    kv = torch.randn(b, sk, 2 * h, d, generator=g).to(torch.bfloat16).to(DEV)
+    k, v = kv[:, :, :h], kv[:, :, h:]                      # a fused projection
+    q = torch.randn(b, h, sq, d, generator=g).to(torch.bfloat16).to(DEV).transpose(1, 2)
+    o, lse = tern.attention(q, k, v)
+    check_forward(q, k, v, None, None, o, lse, "fused and transposed")
+    one = kv[:1].expand(b, sk, 2 * h, d)                   # one caption for all samples
+    mask = (torch.rand(1, sk, generator=g) < 0.7).to(DEV).expand(b, sk)
+    with pytest.raises(ValueError):
+        tern.attention(q, one[:, :, :h], one[:, :, h:], mask=mask.t().contiguous().t())
+    mask = mask.contiguous()
+    o, lse = tern.attention(q, one[:, :, :h], one[:, :, h:], mask=mask.to(torch.uint8))
+    check_forward(q, one[:, :, :h], one[:, :, h:], mask, None, o, lse, "broadcast")
+    wide = torch.zeros(b, sk + 7, dtype=torch.bool, device=DEV)
+    wide[:, 3:sk + 3] = mask
+    o2, _ = tern.attention(q, one[:, :, :h], one[:, :, h:], mask=wide[:, 3:sk + 3])  # a pitch
+    assert torch.equal(o, o2)
+
+
+def test_forward_without_keys_or_queries():
+    q, k, v, _ = make(2, 5, 4, 2, 2, 64, None, seed=1)
+    o, lse = tern.attention(q, k[:, :0], v[:, :0])
+    assert float(o.float().abs().sum()) == 0 and bool(torch.isneginf(lse).all())
+    o, lse = tern.attention(q[:, :0], k, v)
+    assert o.shape == (2, 0, 2, 64) and lse.shape == (2, 2, 0)
+    o, lse = tern.attention(q, k[:, :0], v[:, :0], mask=torch.zeros(2, 0, dtype=torch.bool, device=DEV))
+    assert float(o.float().abs().sum()) == 0
+
+
+def test_forward_long_mask_is_walked_in_parts():
+    # more keys than one workgroup's mask words hold
+    log("attention long mask")
+    b, sk = 1, 70000
+    q, k, v, _ = make(b, 2, sk, 1, 1, 16, None, seed=5)
+    m = torch.zeros(b, sk, dtype=torch.bool, device=DEV)
+    m[:, 40000:40003] = True
+    m[:, sk - 1] = True
+    o, lse = tern.attention(q, k, v, mask=m)
+    check_forward(q, k, v, m, None, o, lse, "long mask")
+    q = torch.cat([q] * 40, 1)
+    o, lse = tern.attention(q, k, v, mask=m)
+    check_forward(q, k, v, m, None, o, lse, "long mask, many rows")
+
+
+def test_refusals():
+    q, k, v, _ = make(2, 5, 6, 4, 2, 64, None, seed=1)
+    for bad, status in (
+            (lambda: tern.attention(q, k, v, scale=0.0), tern.TERN_ERR_ARG),
+            (lambda: tern.attention(q, k, v, scale=float("nan")), tern.TERN_ERR_ARG),
+            (lambda: tern.attention(q[:, :, :3], k, v), tern.TERN_ERR_SHAPE),  # 3 heads on 2
+            (lambda: tern.attention(q[..., :12], k[..., :12], v[..., :12]), tern.TERN_ERR_SHAPE),
+            (lambda: tern.attention(q[..., 1:57], k[..., :56], v[..., :56]), tern.TERN_ERR_ALIGN)):
+        with pytest.raises(tern.TernError) as e:
+            bad()
+        assert e.value.status == status
+    big = torch.zeros(1, 1, 1, 136, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(tern.TernError):
+        tern.attention(big, big, big)
+    for bad in (lambda: tern.attention(q.float(), k, v), lambda: tern.attention(q, k.cpu(), v),
+                lambda: tern.attention(q, k, v, mask=torch.ones(2, 6, device=DEV))):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: tern.attention(q[0], k, v), lambda: tern.attention(q, k, v[:, :5]),
+                lambda: tern.attention(q, k[:1], v[:1]),
+                lambda: tern.attention(q, k, v, mask=torch.ones(2, 5, device=DEV).bool())):
+        with pytest.raises(ValueError):
+            bad()
