@@ -614,6 +614,32 @@ tern_status tern_attention(const tern_heads* q, const tern_heads* k, const tern_
                            const uint8_t* mask, int64_t ldmask, float* lse, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
+/*
+ * tern_attention_bwd: the gradients of tern_attention.  With P = exp(S - lse) over
+ * the kept keys,
+ *   delta = <do, o>,   dS = P (<do, v> - delta),
+ *   dq = scale sum_s dS k,   dk = scale sum_t dS q,   dv = sum_t P do
+ * (dk and dv over the query heads of their key-value head too), fp32 sums in
+ * an order fixed by the sizes (repeated calls give identical bits), P and dS
+ * rounded to bf16 as operands, one rounding of each gradient to bf16.  Gradients of masked
+ * keys are 0.
+ *
+ *   dout   [batch, queries, heads, width] bf16 gradient of o
+ *   q, k, v, mask, shape   as in the forward call
+ *   o, lse  the forward call's outputs
+ *   dq     as q, dk, dv as k and v: outputs
+ *   workspace  at least tern_attention_workspace(shape, mask != NULL, 1) bytes,
+ *          16-byte aligned
+ * Checks as tern_attention; a call without samples or heads is a no-op, one
+ * without queries writes dk = dv = 0, one without keys dq = 0.
+ */
+tern_status tern_attention_bwd(const tern_heads* dout, const tern_heads* q, const tern_heads* k,
+                               const tern_heads* v, const tern_heads* o, const float* lse,
+                               const tern_heads* dq, const tern_heads* dk, const tern_heads* dv,
+                               const tern_attention_shape* shape, const uint8_t* mask,
+                               int64_t ldmask, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
 /* Bytes of workspace that tern_attention (backward == 0) or tern_attention_bwd
  * needs for these sizes (0 for sizes that they refuse). */
 int64_t tern_attention_workspace(const tern_attention_shape* shape, int masked, int backward);

@@ -39,7 +39,7 @@ EXPORTED = ("tern_quantize", "tern_quantize_pack", "tern_pack", "tern_unpack", "
             "tern_gemm_dw", "tern_quantize_act", "tern_pack_a8", "tern_gemm_a8",
             "tern_rope", "tern_residual_norm", "tern_residual_norm_bwd",
             "tern_residual_norm_bwd_workspace", "tern_attention", "tern_attention_workspace",
-            "tern_status_string")
+            "tern_attention_bwd", "tern_status_string")
 
 
 class TernError(RuntimeError):

@@ -49,6 +49,8 @@ _lib.tern_residual_norm_bwd_workspace.restype = ctypes.c_int64
 
 _lib.tern_attention.argtypes = [_bytes] * 5 + [_vp, _i64, _vp, _vp, _i64, _vp]
 _lib.tern_attention.restype = ctypes.c_int
+_lib.tern_attention_bwd.argtypes = [_bytes] * 5 + [_vp] + [_bytes] * 4 + [_vp, _i64, _vp, _i64, _vp]
+_lib.tern_attention_bwd.restype = ctypes.c_int
 _lib.tern_attention_workspace.argtypes = [_bytes, ctypes.c_int, ctypes.c_int]
 _lib.tern_attention_workspace.restype = ctypes.c_int64
 
@@ -281,3 +283,27 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask=None,
         qs, ks, vs, _heads(o, "o", _BF16), shape, mp, ldmask, lse.data_ptr(),
         workspace.data_ptr() if need else None, need, _stream(stream)))
     return o, lse
+
+
+def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       o: torch.Tensor, lse: torch.Tensor, mask=None, scale: float | None = None,
+                       stream=None):
+    """Gradients ``(dq, dk, dv)`` (bf16, contiguous) of ``attention`` from the gradient
+    ``dout`` of ``o``, its arguments and its results ``o`` and ``lse``."""
+    views = [_heads(a, n, _BF16) for a, n in ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (o, "o"))]
+    b, s, h, d = q.shape
+    if dout.shape != q.shape or o.shape != q.shape:
+        raise ValueError("dout and o must have the shape of q")
+    shape = _attention_shape(q, k, v, scale)
+    if not isinstance(lse, torch.Tensor) or not lse.is_cuda or lse.dtype != torch.float32:
+        raise TypeError("lse must be a GPU tensor of dtype torch.float32")
+    if tuple(lse.shape) != (b, h, s) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous [{b}, {h}, {s}] tensor")
+    mp, ldmask = _key_mask(mask, b, k.shape[1])
+    dq, dk, dv = (torch.empty(a.shape, dtype=torch.bfloat16, device=q.device) for a in (q, k, v))
+    need = _lib.tern_attention_workspace(shape, mp is not None, 1)
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check("tern_attention_bwd", _lib.tern_attention_bwd(
+        *views, lse.data_ptr(), *(_heads(a, "gradient", _BF16) for a in (dq, dk, dv)), shape, mp,
+        ldmask, workspace.data_ptr(), need, _stream(stream)))
+    return dq, dk, dv

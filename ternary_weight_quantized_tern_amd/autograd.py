@@ -126,3 +126,29 @@ def block_boundary(r, y=None, *, gate=None, scale=None, shift=None, tokens=None,
     r_out, h = BlockBoundaryFunction.apply(r, y, gate, scale, shift, pre_weight, post_weight,
                                            options)
     return h if y is None else r_out if pre is None else (r_out, h)
+
+
+class AttentionFunction(torch.autograd.Function):
+    """Attention to keys of another length (tern_attention) with the gradients
+    of tern_attention_bwd; the mask has none."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, mask, scale):
+        o, lse = _k.attention(q.detach(), k.detach(), v.detach(), mask, scale)
+        ctx.save_for_backward(q.detach(), k.detach(), v.detach(), mask, o, lse)
+        ctx.scale = scale
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, mask, o, lse = ctx.saved_tensors
+        do = do.to(torch.bfloat16)
+        if do.stride(-1) != 1 or any(s % 8 for s in do.stride()[:-1]):
+            do = do.contiguous()
+        return (*_k.attention_backward(do, q, k, v, o, lse, mask, ctx.scale), None, None)
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask=None,
+                    scale: float | None = None) -> torch.Tensor:
+    """``attention`` with gradients: ``o`` alone."""
+    return AttentionFunction.apply(q, k, v, mask, scale)

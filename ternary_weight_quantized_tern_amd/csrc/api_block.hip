@@ -77,8 +77,9 @@ tern_status check_view(const tern_heads* v, int64_t batch, int64_t tokens, int64
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The sizes' part of the kernel's parameters (all that the workspace depends on).
-void fill_shape(tern::AttentionParams& p, const tern_attention_shape& s) {
+// The sizes' part of a kernel's parameters (all that the workspace depends on).
+template <typename Params>
+void fill_shape(Params& p, const tern_attention_shape& s) {
   p.b = static_cast<int32_t>(s.batch);
   p.sq = static_cast<int32_t>(s.queries);
   p.sk = s.keys;
@@ -283,11 +284,17 @@ tern_status tern_residual_norm_bwd(const tern_residual_norm_args* args, const vo
 
 int64_t tern_attention_workspace(const tern_attention_shape* shape, int masked, int backward) {
   if (check_attention(shape) != TERN_OK || shape->batch == 0 || shape->heads == 0) return 0;
+  // (The plan depends on whether there is a mask, not on the mask.)
+  const uint8_t* mask = masked ? reinterpret_cast<const uint8_t*>(1) : nullptr;
+  if (backward) {
+    tern::AttentionBwdParams p = {};
+    fill_shape(p, *shape);
+    p.mask = mask;
+    return tern::attention_bwd_workspace(p);
+  }
   tern::AttentionParams p = {};
   fill_shape(p, *shape);
-  // (The plan depends on whether there is a mask, not on the mask.)
-  p.mask = masked ? reinterpret_cast<const uint8_t*>(1) : nullptr;
-  (void)backward;
+  p.mask = mask;
   return shape->queries == 0 ? 0 : tern::attention_workspace(p);
 }
 
@@ -329,6 +336,58 @@ tern_status tern_attention(const tern_heads* q, const tern_heads* k, const tern_
   p.lse = lse;
   p.ldmask = ldmask;
   return from_hip(tern::launch_attention(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+tern_status tern_attention_bwd(const tern_heads* dout, const tern_heads* q, const tern_heads* k,
+                               const tern_heads* v, const tern_heads* o, const float* lse,
+                               const tern_heads* dq, const tern_heads* dk, const tern_heads* dv,
+                               const tern_attention_shape* shape, const uint8_t* mask,
+                               int64_t ldmask, void* workspace, int64_t workspace_bytes,
+                               void* stream) {
+  const tern_status bad = check_attention(shape);
+  if (bad != TERN_OK) return bad;
+  const tern_attention_shape& s = *shape;
+  if (s.batch == 0 || s.heads == 0 || (s.queries == 0 && s.keys == 0)) return TERN_OK;
+  tern::AttentionBwdParams p = {};
+  fill_shape(p, s);
+  p.mask = mask;
+  const int64_t need = tern::attention_bwd_workspace(p);
+  if (workspace_bytes < need) return TERN_ERR_SHAPE;
+  static const tern_heads none = {};
+  if (s.queries == 0) dout = q = o = dq = &none;
+  if (s.keys == 0) k = v = dk = dv = &none;
+  const tern_heads* views[8] = {dout, q, o, dq, k, v, dk, dv};
+  for (int i = 0; i < 8; ++i) {
+    if (views[i] == nullptr) return TERN_ERR_NULL;
+    if (views[i]->data == nullptr && (i < 4 ? s.queries : s.keys) > 0) return TERN_ERR_NULL;
+  }
+  if ((s.queries > 0 && lse == nullptr) || (need > 0 && workspace == nullptr)) return TERN_ERR_NULL;
+  if (mask != nullptr && ldmask < s.keys) return TERN_ERR_STRIDE;
+  for (int i = 0; i < 8; ++i) {
+    const tern_status st = check_view(views[i], s.batch, i < 4 ? s.queries : s.keys,
+                                      i < 4 ? s.heads : s.kv_heads);
+    if (st != TERN_OK) return st;
+  }
+  if (!aligned(lse, 4) || (need > 0 && !aligned(workspace, 16))) return TERN_ERR_ALIGN;
+  p.dout = static_cast<const uint16_t*>(dout->data);
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.k = static_cast<const uint16_t*>(k->data);
+  p.v = static_cast<const uint16_t*>(v->data);
+  p.o = static_cast<const uint16_t*>(o->data);
+  p.dq = static_cast<uint16_t*>(dq->data);
+  p.dk = static_cast<uint16_t*>(dk->data);
+  p.dv = static_cast<uint16_t*>(dv->data);
+  fill_view(dout, s.batch, s.queries, s.heads, p.dob, p.dot, p.doh);
+  fill_view(q, s.batch, s.queries, s.heads, p.qb, p.qt, p.qh);
+  fill_view(o, s.batch, s.queries, s.heads, p.ob, p.ot, p.oh);
+  fill_view(dq, s.batch, s.queries, s.heads, p.dqb, p.dqt, p.dqh);
+  fill_view(k, s.batch, s.keys, s.kv_heads, p.kb, p.kt, p.kh);
+  fill_view(v, s.batch, s.keys, s.kv_heads, p.vb, p.vt, p.vh);
+  fill_view(dk, s.batch, s.keys, s.kv_heads, p.dkb, p.dkt, p.dkh);
+  fill_view(dv, s.batch, s.keys, s.kv_heads, p.dvb, p.dvt, p.dvh);
+  p.lse = lse;
+  p.ldmask = ldmask;
+  return from_hip(tern::launch_attention_bwd(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

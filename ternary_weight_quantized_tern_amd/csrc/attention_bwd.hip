@@ -1,0 +1,529 @@
+// Gradients of attention to keys of another length.  With P = exp(S - lse) of the
+// kept keys, recomputed from q, k and the stored lse,
+//   delta = <do, o>,  dS = P (do v^T - delta),
+//   dq = scale dS k,  dk = scale dS^T q,  dv = P^T do.
+//
+// Two kernels, seven products in all: one by query rows (S, dP, dq), one by keys
+// (S, dP, dv, dk).  A single pass would need five, but then one of dq and dk, dv
+// is summed by workgroups in no fixed order; here every sum has one owner and a
+// fixed order, with no atomics, and a shared key-value head's sum over its query
+// heads is simply more rows of the loop.
+//
+// By rows: as the forward kernel, S^T = K q^T and dP^T = V do^T put a row in each
+// lane's column, dS^T is the B operand of dq^T = K^T dS^T; q and do stay in
+// registers, K is read from LDS by rows and transposed, V by rows.  It also
+// forms delta and the row's log2-sum-exp for the second kernel.
+// By keys: S = Q k^T and dP = dO v^T put a key in each lane's column, P and dS
+// are the B operands of dv^T = dO^T P and dk^T = Q^T dS; k and v stay in
+// registers, Q and dO are read from LDS by rows and transposed.  Products of a masked key
+// stay in its column, which is not stored.
+// Where there are too few workgroups, the loop is split among several, whose
+// fp32 sums a last kernel adds in order.
+// P and dS are rounded to bf16 as operands; S, dP, delta and all sums are fp32.
+#include "attention_common.h"
+
+namespace tern {
+namespace {
+
+[[maybe_unused]] constexpr float kLog2e = 1.4426950408889634f;
+
+// Column i of a transposed accumulator (channels down, as 32 dt + (e & 3) + 8 (e >> 2)
+// + 4 h) times `factor`: eight consecutive channels a lane after the halves trade.
+template <int DT>
+__device__ inline void store_bf16(const f32x16_t (&acc)[DT], float factor, uint16_t* out, int h,
+                                  int d, bool live) {
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = 4 * g + 2 * x;
+        const bf16x2_t two = {static_cast<__bf16>(acc[t][e] * factor),
+                              static_cast<__bf16>(acc[t][e + 1] * factor)};
+        w[x] = __builtin_bit_cast(uint32_t, two);
+      }
+      const auto a0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+      const auto a1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+      const int c = 32 * t + 8 * g + 8 * h;
+      const u32x4_t v = {a0[0], a1[0], a0[1], a1[1]};
+      if (live && c < d) *reinterpret_cast<u32x4_t*>(out + c) = v;
+    }
+}
+
+template <int DT>
+__device__ inline void store_f32(const f32x16_t (&acc)[DT], float factor, float* out, int h, int d,
+                                 bool live) {
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = 32 * t + 8 * g + 4 * h;
+      if (live && c < d)
+        *reinterpret_cast<f32x4_t*>(out + c) =
+            f32x4_t{acc[t][4 * g] * factor, acc[t][4 * g + 1] * factor, acc[t][4 * g + 2] * factor,
+                    acc[t][4 * g + 3] * factor};
+    }
+}
+
+template <int CPR, bool MASK>
+__global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = 4, BK = 64, DS = CPR / 2, DT = (CPR + 3) / 4;
+  constexpr uint32_t kBytes = tile_bytes<CPR>(BK);
+  __shared__ __attribute__((aligned(1024))) uint8_t k0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t k1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t v0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t v1[kBytes];
+  __shared__ unsigned long long words[MASK ? kMaskWords : 1];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 31, h = lane >> 5;
+
+  uint32_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int block = at % p.row_blocks;
+  at /= p.row_blocks;
+  const int split = at % p.dq_splits;
+  const uint32_t bh = at / p.dq_splits;
+  const int hk = bh % p.hkv, b = bh / p.hkv;
+
+  const int t_first = split * p.key_tiles_per_split;
+  const int t_end = t_first + p.key_tiles_per_split < p.key_tiles ? t_first + p.key_tiles_per_split
+                                                                  : p.key_tiles;
+  if (MASK) {
+    mask_words(words, p.mask + b * p.ldmask, static_cast<int64_t>(t_first) * BK, p.sk,
+               t_end - t_first, wave, NW, lane);
+    __syncthreads();
+  }
+
+  const int row = (block * NW + wave) * 32 + i;
+  const PackedRow pr = packed_row(row, p.rows, p.sq);
+  const int head = hk * p.group + pr.head;
+  bf16x8_t qf[DS], dof[DS];
+  float delta = 0.0f;
+  {
+    const uint16_t* q = p.q + b * p.qb + static_cast<int64_t>(pr.token) * p.qt +
+                        static_cast<int64_t>(head) * p.qh;
+    const uint16_t* dout = p.dout + b * p.dob + static_cast<int64_t>(pr.token) * p.dot +
+                           static_cast<int64_t>(head) * p.doh;
+    const uint16_t* o = p.o + b * p.ob + static_cast<int64_t>(pr.token) * p.ot +
+                        static_cast<int64_t>(head) * p.oh;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const int c = 16 * s + 8 * h;
+      qf[s] = dof[s] = bf16x8_t{};
+      if (pr.live && c < p.d) {
+        qf[s] = *reinterpret_cast<const bf16x8_t*>(q + c);
+        dof[s] = *reinterpret_cast<const bf16x8_t*>(dout + c);
+        const bf16x8_t of = *reinterpret_cast<const bf16x8_t*>(o + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          delta = __builtin_fmaf(static_cast<float>(dof[s][e]), static_cast<float>(of[e]), delta);
+      }
+    }
+    float lo, hi;
+    halves(delta, lo, hi);
+    delta = lo + hi;
+  }
+  const int64_t stat = (static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + pr.token;
+  float lse2 = pr.live ? p.lse[stat] * kLog2e : INFINITY;
+  if (lse2 == -INFINITY) lse2 = INFINITY;  // a row without keys: P = 0
+  if (pr.live && h == 0 && split == 0) {
+    p.lse2[stat] = lse2;
+    p.delta[stat] = delta;
+  }
+
+  const uint16_t* kbase = p.k + b * p.kb + hk * p.kh;
+  const uint16_t* vbase = p.v + b * p.vb + hk * p.vh;
+  TileCopy<CPR, BK, NW> kcopy, vcopy;
+  kcopy.plan(wave, lane, p.kt, p.d);
+  vcopy.plan(wave, lane, p.vt, p.d);
+  uint32_t roff[DS], toffa[DT], toffb[DT];
+#pragma unroll
+  for (int s = 0; s < DS; ++s) roff[s] = tile_offset<CPR>(i, 2 * s + h);
+#pragma unroll
+  for (int t = 0; t < DT; ++t) transposed_offsets<CPR>(lane, t, toffa[t], toffb[t]);
+
+  auto word_of = [&](int t) -> unsigned long long {
+    if (MASK) return uniform64(words[t - t_first]);
+    return tail_word(static_cast<int64_t>(t) * BK, p.sk);
+  };
+  auto next_tile = [&](int t) {
+    if (MASK)
+      while (t < t_end && word_of(t) == 0) ++t;
+    return t;
+  };
+  auto issue = [&](int t, uint8_t* kl, uint8_t* vl) {
+    const unsigned long long w = word_of(t);
+    auto keep = [&](uint32_t r) { return ((w >> r) & 1ull) != 0; };
+    kcopy.issue(kbase + static_cast<int64_t>(t) * BK * p.kt, kl, wave, lane, w == ~0ull, keep);
+    vcopy.issue(vbase + static_cast<int64_t>(t) * BK * p.vt, vl, wave, lane, w == ~0ull, keep);
+  };
+
+  f32x16_t dq[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dq[t] = f32x16_t{};
+
+  auto compute = [&](int t, const uint8_t* kl, const uint8_t* vl) {
+    const unsigned long long w = word_of(t);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+      for (int c = 0; c < DS; ++c) {
+        s = mfma32(read_rows(kl, roff[c] + u * (32 * CPR * 16u)), qf[c], s);
+        dp = mfma32(read_rows(vl, roff[c] + u * (32 * CPR * 16u)), dof[c], dp);
+      }
+      const uint32_t part = static_cast<uint32_t>(w >> (32 * u));
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], p.scale_log2, -lse2)) * (dp[e] - delta);
+      if (part != 0xFFFFFFFFu) {
+        const uint32_t mine = part >> (4 * h);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          x[e] = (mine >> ((e & 3) + 8 * (e >> 2))) & 1u ? x[e] : 0.0f;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8_t ds = to_operand(x + 8 * c);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          dq[d] = mfma32(read_transposed(kl, toffa[d] + (2 * u + c) * (16 * CPR * 16u),
+                                         toffb[d] + (2 * u + c) * (16 * CPR * 16u)),
+                         ds, dq[d]);
+      }
+    }
+  };
+
+  int t = next_tile(t_first);
+  if (t < t_end) issue(t, k0, v0);
+  while (t < t_end) {
+    wait_vmem();
+    tile_barrier();
+    int n = next_tile(t + 1);
+    if (n < t_end) issue(n, k1, v1);
+    compute(t, k0, v0);
+    t = n;
+    if (t >= t_end) break;
+    wait_vmem();
+    tile_barrier();
+    n = next_tile(t + 1);
+    if (n < t_end) issue(n, k0, v0);
+    compute(t, k1, v1);
+    t = n;
+  }
+
+  if (p.dq_splits > 1) {
+    const int64_t r = (static_cast<int64_t>(split) * p.b * p.hkv + bh) * p.rows + row;
+    store_f32<DT>(dq, p.scale, p.part_dq + r * p.d, h, p.d, pr.live);
+  } else {
+    store_bf16<DT>(dq, p.scale,
+                   p.dq + b * p.dqb + static_cast<int64_t>(pr.token) * p.dqt +
+                       static_cast<int64_t>(head) * p.dqh,
+                   h, p.d, pr.live);
+  }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+template <int CPR, bool MASK>
+__global__ __launch_bounds__(256, CPR > 10 ? 1 : 2) void attention_dkv_kernel(
+    AttentionBwdParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = 4, BR = 64, DS = CPR / 2, DT = (CPR + 3) / 4;
+  constexpr uint32_t kBytes = tile_bytes<CPR>(BR);
+  __shared__ __attribute__((aligned(1024))) uint8_t q0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t q1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t o0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t o1[kBytes];
+  // lse2 and delta of a tile's rows.
+  __shared__ __attribute__((aligned(1024))) float st0[2 * BR];
+  __shared__ __attribute__((aligned(1024))) float st1[2 * BR];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 31, h = lane >> 5;
+
+  uint32_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int block = at % p.key_blocks;
+  at /= p.key_blocks;
+  const int split = at % p.dkv_splits;
+  const uint32_t bh = at / p.dkv_splits;
+  const int hk = bh % p.hkv, b = bh / p.hkv;
+
+  const int64_t key = (static_cast<int64_t>(block) * NW + wave) * 32 + i;
+  const bool in = key < p.sk;
+  int t_first = split * p.row_tiles_per_split;
+  int t_end = t_first + p.row_tiles_per_split < p.row_tiles ? t_first + p.row_tiles_per_split
+                                                            : p.row_tiles;
+  bool kept = in;
+  if (MASK) {
+    const uint8_t* mask = p.mask + b * p.ldmask;
+    kept = in && mask[key] != 0;
+    const int64_t first = static_cast<int64_t>(block) * (32 * NW);
+    const bool any = (first + lane < p.sk && mask[first + lane] != 0) ||
+                     (first + 64 + lane < p.sk && mask[first + 64 + lane] != 0);
+    if (__ballot(any) == 0) t_end = t_first;  // the same in every wave: nothing to add
+  }
+
+  // The keys and values of this lane's column (zeros where they do not count).
+  bf16x8_t kf[DS], vf[DS];
+  {
+    const uint16_t* k = p.k + b * p.kb + hk * p.kh + key * p.kt;
+    const uint16_t* v = p.v + b * p.vb + hk * p.vh + key * p.vt;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const int c = 16 * s + 8 * h;
+      kf[s] = vf[s] = bf16x8_t{};
+      if (kept && c < p.d) {
+        kf[s] = *reinterpret_cast<const bf16x8_t*>(k + c);
+        vf[s] = *reinterpret_cast<const bf16x8_t*>(v + c);
+      }
+    }
+  }
+
+  TileCopy<CPR, BR, NW> qcopy, ocopy;
+  qcopy.plan(wave, lane, p.qt, p.d);
+  ocopy.plan(wave, lane, p.dot, p.d);
+  uint32_t roff[DS], toffa[DT], toffb[DT];
+#pragma unroll
+  for (int s = 0; s < DS; ++s) roff[s] = tile_offset<CPR>(i, 2 * s + h);
+#pragma unroll
+  for (int t = 0; t < DT; ++t) transposed_offsets<CPR>(lane, t, toffa[t], toffb[t]);
+
+  // Row tile t: head t / tiles_per_head of the group, 64 tokens.
+  auto issue = [&](int t, uint8_t* ql, uint8_t* ol, float* st) {
+    const int g = t / p.tiles_per_head;
+    const int64_t token = static_cast<int64_t>(t - g * p.tiles_per_head) * BR;
+    const int head = hk * p.group + g;
+    const int left = p.sq - static_cast<int>(token);
+    auto keep = [&](uint32_t r) { return static_cast<int>(r) < left; };
+    qcopy.issue(p.q + b * p.qb + head * p.qh + token * p.qt, ql, wave, lane, left >= BR, keep);
+    ocopy.issue(p.dout + b * p.dob + head * p.doh + token * p.dot, ol, wave, lane, left >= BR,
+                keep);
+    if (wave < 2) {
+      const float* src = (wave == 0 ? p.lse2 : p.delta) +
+                         (static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + token;
+      const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(src, 4u * (left < BR ? left : BR));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)(st + wave * BR), 4, 4 * lane, 0,
+                                               0, 0);
+    }
+  };
+
+  f32x16_t dk[DT], dv[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dk[t] = dv[t] = f32x16_t{};
+
+  auto compute = [&](const uint8_t* ql, const uint8_t* ol, const float* st) {
+#pragma unroll
+    for (int u = 0; u < BR / 32; ++u) {
+      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+      for (int c = 0; c < DS; ++c) {
+        s = mfma32(read_rows(ql, roff[c] + u * (32 * CPR * 16u)), kf[c], s);
+        dp = mfma32(read_rows(ol, roff[c] + u * (32 * CPR * 16u)), vf[c], dp);
+      }
+      float x[16], y[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t lse2 = *reinterpret_cast<const f32x4_t*>(st + 32 * u + 8 * g + 4 * h);
+        const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(st + BR + 32 * u + 8 * g + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * g + e;
+          x[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], p.scale_log2, -lse2[e]));
+          y[r] = x[r] * (dp[r] - delta[e]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8_t pf = to_operand(x + 8 * c), df = to_operand(y + 8 * c);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const uint32_t a = toffa[d] + (2 * u + c) * (16 * CPR * 16u);
+          const uint32_t q = toffb[d] + (2 * u + c) * (16 * CPR * 16u);
+          dv[d] = mfma32(read_transposed(ol, a, q), pf, dv[d]);
+          dk[d] = mfma32(read_transposed(ql, a, q), df, dk[d]);
+        }
+      }
+    }
+  };
+
+  int t = t_first;
+  if (t < t_end) issue(t, q0, o0, st0);
+  while (t < t_end) {
+    wait_vmem();
+    tile_barrier();
+    if (t + 1 < t_end) issue(t + 1, q1, o1, st1);
+    compute(q0, o0, st0);
+    if (++t >= t_end) break;
+    wait_vmem();
+    tile_barrier();
+    if (t + 1 < t_end) issue(t + 1, q0, o0, st0);
+    compute(q1, o1, st1);
+    ++t;
+  }
+
+  if (!kept) {
+#pragma unroll
+    for (int t2 = 0; t2 < DT; ++t2) dk[t2] = dv[t2] = f32x16_t{};
+  }
+  if (p.dkv_splits > 1) {
+    const int64_t r = (static_cast<int64_t>(split) * p.b * p.hkv + bh) * p.sk + key;
+    store_f32<DT>(dk, p.scale, p.part_dk + r * p.d, h, p.d, in);
+    store_f32<DT>(dv, 1.0f, p.part_dv + r * p.d, h, p.d, in);
+  } else {
+    store_bf16<DT>(dk, p.scale, p.dk + b * p.dkb + key * p.dkt + hk * p.dkh, h, p.d, in);
+    store_bf16<DT>(dv, 1.0f, p.dv + b * p.dvb + key * p.dvt + hk * p.dvh, h, p.d, in);
+  }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// The splits' sums of one gradient, added in order: eight channels a thread.
+// rows = heads_per_kv * tokens rows of each (sample, kv head).
+__global__ __launch_bounds__(256) void attention_add_kernel(const float* part, int splits,
+                                                            uint16_t* out, int64_t ob, int64_t ot,
+                                                            int64_t oh, int hkv, int group,
+                                                            int64_t tokens, int64_t total, int d) {
+  const int chunks = d / 8;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (x >= total * chunks) return;
+  const int64_t r = x / chunks;
+  const int c = static_cast<int>(x - r * chunks) * 8;
+  float sum[8] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float* in = part + (s * total + r) * d + c;
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(in);
+    const f32x4_t b = *reinterpret_cast<const f32x4_t*>(in + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum[e] += a[e];
+      sum[4 + e] += b[e];
+    }
+  }
+  const int64_t head = r / tokens, token = r - head * tokens;  // over sample, kv head, group
+  const int64_t heads = static_cast<int64_t>(hkv) * group;
+  const int64_t b = head / heads;
+  *reinterpret_cast<bf16x8_t*>(out + b * ob + token * ot + (head - b * heads) * oh + c) =
+      to_operand(sum);
+}
+
+struct BwdPlan {
+  int row_blocks, key_tiles, key_tiles_per_split, dq_splits;
+  int key_blocks, tiles_per_head, row_tiles, row_tiles_per_split, dkv_splits;
+  int64_t stats, part_dq, part_dkv;  // floats
+};
+
+// `tiles` steps of a loop among `wanted / base` workgroups, at least `least` each.
+void split(int64_t tiles, int64_t base, int64_t wanted, int least, int64_t most, int* per,
+           int* splits) {
+  int64_t n = base > 0 ? wanted / base : 1;
+  if (n > tiles / least) n = tiles / least;
+  if (n < 1) n = 1;
+  if (n < (tiles + most - 1) / most) n = (tiles + most - 1) / most;
+  int64_t each = (tiles + n - 1) / n;
+  if (each < 1) each = 1;
+  *per = static_cast<int>(each);
+  *splits = static_cast<int>(tiles > 0 ? (tiles + each - 1) / each : 1);
+}
+
+BwdPlan plan(const AttentionBwdParams& p) {
+  BwdPlan r;
+  const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
+  r.row_blocks = (p.rows + 127) / 128;
+  r.key_tiles = static_cast<int>((p.sk + 63) / 64);
+  split(r.key_tiles, bh * r.row_blocks, 512, 4, p.mask ? kMaskWords : int64_t(1) << 30,
+        &r.key_tiles_per_split, &r.dq_splits);
+  r.key_blocks = static_cast<int>((p.sk + 127) / 128);
+  r.tiles_per_head = (p.sq + 63) / 64;
+  r.row_tiles = r.tiles_per_head * p.group;
+  split(r.row_tiles, bh * r.key_blocks, p.d > 80 ? 256 : 512, 4, int64_t(1) << 30,
+        &r.row_tiles_per_split, &r.dkv_splits);
+  auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
+  r.stats = whole(bh * p.rows);
+  r.part_dq = r.dq_splits > 1 ? whole(r.dq_splits * bh * p.rows * p.d) : 0;
+  r.part_dkv = r.dkv_splits > 1 ? whole(r.dkv_splits * bh * p.sk * p.d) : 0;
+  return r;
+}
+
+template <int CPR>
+hipError_t launch(const AttentionBwdParams& p, hipStream_t stream) {
+  const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
+  const int64_t by_rows = bh * p.row_blocks * p.dq_splits;
+  const int64_t by_keys = bh * p.key_blocks * p.dkv_splits;
+  if (by_rows > 0x7FFFFFFF || by_keys > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (by_rows > 0) {
+    const dim3 g(static_cast<unsigned>(by_rows));
+    if (p.mask)
+      hipLaunchKernelGGL((attention_dq_kernel<CPR, true>), g, dim3(256), 0, stream, p);
+    else
+      hipLaunchKernelGGL((attention_dq_kernel<CPR, false>), g, dim3(256), 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (by_keys > 0) {
+    const dim3 g(static_cast<unsigned>(by_keys));
+    if (p.mask)
+      hipLaunchKernelGGL((attention_dkv_kernel<CPR, true>), g, dim3(256), 0, stream, p);
+    else
+      hipLaunchKernelGGL((attention_dkv_kernel<CPR, false>), g, dim3(256), 0, stream, p);
+  }
+  return hipGetLastError();
+}
+
+hipError_t add(const float* part, int splits, uint16_t* out, int64_t ob, int64_t ot, int64_t oh,
+               int hkv, int group, int64_t tokens, int64_t total, int d, hipStream_t stream) {
+  const int64_t blocks = (total * (d / 8) + 255) / 256;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(attention_add_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                     stream, part, splits, out, ob, ot, oh, hkv, group, tokens, total, d);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t attention_bwd_workspace(const AttentionBwdParams& p) {
+  const BwdPlan r = plan(p);
+  return (2 * r.stats + r.part_dq + 2 * r.part_dkv) * 4;
+}
+
+hipError_t launch_attention_bwd(AttentionBwdParams& p, void* workspace, hipStream_t stream) {
+  const BwdPlan r = plan(p);
+  p.row_blocks = r.row_blocks;
+  p.key_tiles = r.key_tiles;
+  p.key_tiles_per_split = r.key_tiles_per_split;
+  p.dq_splits = r.dq_splits;
+  p.key_blocks = r.key_blocks;
+  p.tiles_per_head = r.tiles_per_head;
+  p.row_tiles = r.row_tiles;
+  p.row_tiles_per_split = r.row_tiles_per_split;
+  p.dkv_splits = r.dkv_splits;
+  float* w = static_cast<float*>(workspace);
+  p.lse2 = w;
+  p.delta = w + r.stats;
+  p.part_dq = w + 2 * r.stats;
+  p.part_dk = p.part_dq + r.part_dq;
+  p.part_dv = p.part_dk + r.part_dkv;
+  hipError_t e = p.d <= 32   ? launch<4>(p, stream)
+                 : p.d <= 64 ? launch<8>(p, stream)
+                 : p.d <= 80 ? launch<10>(p, stream)
+                 : p.d <= 96 ? launch<12>(p, stream)
+                             : launch<16>(p, stream);
+  const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
+  if (e == hipSuccess && r.dq_splits > 1 && p.rows > 0)
+    e = add(p.part_dq, r.dq_splits, p.dq, p.dqb, p.dqt, p.dqh, p.hkv, p.group, p.sq, bh * p.rows,
+            p.d, stream);
+  if (e == hipSuccess && r.dkv_splits > 1 && p.sk > 0) {
+    e = add(p.part_dk, r.dkv_splits, p.dk, p.dkb, p.dkt, p.dkh, p.hkv, 1, p.sk, bh * p.sk, p.d,
+            stream);
+    if (e == hipSuccess)
+      e = add(p.part_dv, r.dkv_splits, p.dv, p.dvb, p.dvt, p.dvh, p.hkv, 1, p.sk, bh * p.sk, p.d,
+              stream);
+  }
+  return e;
+}
+
+}  // namespace tern

@@ -168,4 +168,26 @@ struct AttentionParams {
 int64_t attention_workspace(const AttentionParams& params);
 hipError_t launch_attention(AttentionParams& params, void* workspace, hipStream_t stream);
 
+// Its gradients; strides as above, of do (dob ..) and the outputs too.
+struct AttentionBwdParams {
+  const uint16_t *dout, *q, *k, *v, *o;
+  int64_t dob, dot, doh, qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh;
+  const float* lse;
+  uint16_t *dq, *dk, *dv;
+  int64_t dqb, dqt, dqh, dkb, dkt, dkh, dvb, dvt, dvh;
+  const uint8_t* mask;
+  int64_t ldmask;
+  int32_t b, sq, hkv, group, d, rows;
+  int64_t sk;
+  float scale, scale_log2;
+
+  // By query rows: blocks of 128 rows, tiles of 64 keys.  By keys: blocks of
+  // 128 keys, tiles of 64 rows of one head.
+  int32_t row_blocks, key_tiles, key_tiles_per_split, dq_splits;
+  int32_t key_blocks, tiles_per_head, row_tiles, row_tiles_per_split, dkv_splits;
+  float *lse2, *delta, *part_dq, *part_dk, *part_dv;  // in the workspace
+};
+int64_t attention_bwd_workspace(const AttentionBwdParams& params);
+hipError_t launch_attention_bwd(AttentionBwdParams& params, void* workspace, hipStream_t stream);
+
 }  // namespace tern

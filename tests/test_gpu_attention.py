@@ -234,3 +234,155 @@ def test_refusals():
                 lambda: tern.attention(q, k, v, mask=torch.ones(2, 5, device=DEV).bool())):
         with pytest.raises(ValueError):
             bad()
+
+
+def check_backward(do, q, k, v, mask, scale, o, lse, got, what):
+    """The gradients against the formulas of the stored o and lse in 64 bits."""
+    hkv = k.shape[2]
+    scale = 1 / math.sqrt(q.shape[3]) if scale is None else scale
+    b, sq, hq, d = q.shape
+    s, err = logits(q, k, mask, scale)
+    qd, kd, vd = group(q, hkv), group(k, hkv), group(v, hkv)
+    dod, od = group(do, hkv), group(o, hkv)
+    l = lse.double().view(b, hkv, hq // hkv, sq, 1)
+    p = torch.where(torch.isneginf(s) | torch.isneginf(l), 0.0,
+                    torch.exp(s - torch.where(torch.isneginf(l), 0.0, l)))
+    dp = dod @ vd.transpose(-1, -2)
+    delta = (dod * od).sum(-1, keepdim=True)
+    ds = p * (dp - delta)
+    # relative error of P: the logits', and exp and lse in fp32
+    rel = 2 * err + 2.0 ** -16 * (1 + torch.where(torch.isneginf(l), 0.0, l.abs()))
+    fp32 = 2.0 ** -17 * p * (dod.abs() @ vd.abs().transpose(-1, -2)
+                             + (dod.abs() * od.abs()).sum(-1, keepdim=True))
+    dsize = ds.abs() * (U + rel) + fp32
+    psize = p * (U + rel)
+    dq, dk, dv = got
+    ref = ungroup(scale * (ds @ kd))
+    within(dq, ref, ungroup(scale * (dsize @ kd.abs())) + U * ref.abs(), what + ": dq")
+    for name, grad, m, msize, rows, f in (("dk", dk, ds, dsize, qd, scale),
+                                          ("dv", dv, p, psize, dod, 1.0)):
+        ref = f * (m.transpose(-1, -2) @ rows).sum(2, keepdim=True)
+        size = f * (msize.transpose(-1, -2) @ rows.abs()).sum(2, keepdim=True)
+        within(grad, ungroup(ref), ungroup(size + U * ref.abs()), what + ": " + name)
+
+
+BACKWARD = [
+    # b, sq, sk, hq, hkv, d, mask
+    (1, 1, 1, 1, 1, 8, None),
+    (2, 1, 300, 8, 2, 64, "random"),
+    (1, 3, 3000, 2, 2, 128, "prefix"),      # keys split among workgroups
+    (2, 200, 77, 16, 16, 72, "prefix"),
+    (1, 1500, 40, 2, 1, 128, "random"),     # rows split among workgroups
+    (2, 130, 129, 6, 2, 40, "random"),
+    (1, 65, 64, 3, 3, 32, None),
+    (1, 300, 513, 4, 2, 96, None),
+    (2, 257, 320, 4, 4, 80, "suffix"),
+    (3, 50, 128, 6, 2, 24, "one"),
+    (2, 70, 90, 2, 2, 64, "none_kept"),
+    (1, 256, 256, 8, 8, 128, None),
+    (1, 190, 200, 4, 1, 128, "suffix"),
+]
+
+
+@pytest.mark.parametrize("b,sq,sk,hq,hkv,d,mask", BACKWARD)
+def test_backward_matches_the_formulas(b, sq, sk, hq, hkv, d, mask):
+    log(f"attention_backward b={b} sq={sq} sk={sk} hq={hq} hkv={hkv} d={d} mask={mask}")
+    q, k, v, m = make(b, sq, sk, hq, hkv, d, mask, seed=2 * sq + sk + d)
+    g = torch.Generator().manual_seed(sq + sk)
+    do = torch.randn(b, sq, hq, d, generator=g).to(torch.bfloat16).to(DEV)
+    o, lse = tern.attention(q, k, v, mask=m)
+    got = tern.attention_backward(do, q, k, v, o, lse, mask=m)
+    torch.cuda.synchronize()
+    check_backward(do, q, k, v, m, None, o, lse, got, f"{b} {sq} {sk} {hq} {hkv} {d} {mask}")
+    again = tern.attention_backward(do, q, k, v, o, lse, mask=m)
+    assert all(torch.equal(a, b2) for a, b2 in zip(got, again))
+    if m is not None:
+        assert float(got[1].float()[~m].abs().sum()) == 0
+        assert float(got[2].float()[~m].abs().sum()) == 0
+
+
+@pytest.mark.parametrize("sq", [3, 140])
+def test_backward_ignores_what_masked_keys_hold(sq):
+    log(f"attention_backward masked NaN sq={sq}")
+    q, k, v, m = make(2, sq, 333, 4, 2, 72, "random", seed=12)
+    m[1] = False  # a dropped caption
+    do = torch.randn(q.shape, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    o, lse = tern.attention(q, k, v, mask=m)
+    clean = tern.attention_backward(do, q, k, v, o, lse, mask=m)
+    assert all(bool(torch.isfinite(x).all()) for x in clean)
+    for bad in (float("nan"), float("inf"), torch.finfo(torch.bfloat16).min):
+        kb = torch.where(m[:, :, None, None], k, torch.full_like(k, bad))
+        vb = torch.where(m[:, :, None, None], v, torch.full_like(v, bad))
+        got = tern.attention_backward(do, q, kb, vb, o, lse, mask=m)
+        assert all(torch.equal(a, b) for a, b in zip(got, clean)), bad
+
+
+def test_backward_strides_and_broadcast_through_autograd():
+    log("attention autograd strides")
+    g = torch.Generator().manual_seed(3)
+    b, sq, sk, h, d = 2, 70, 100, 3, 64
+    kv = torch.randn(1, sk, 2 * h, d, generator=g).to(torch.bfloat16).to(DEV).requires_grad_()
+    qkv = torch.randn(b, h, sq, d, generator=g).to(torch.bfloat16).to(DEV).requires_grad_()
+    mask = (torch.rand(b, sk, generator=g) < 0.7).to(DEV)
+    both = kv.expand(b, sk, 2 * h, d)
+    q = qkv.transpose(1, 2)
+    o = tern.cross_attention(q, both[:, :, :h], both[:, :, h:], mask=mask)
+    do = torch.randn(b, h, sq, d, generator=g).to(torch.bfloat16).to(DEV).transpose(1, 2)
+    o.backward(do)
+    with torch.no_grad():
+        k, v = both[:, :, :h], both[:, :, h:]
+        o2, lse = tern.attention(q, k, v, mask=mask)
+        got = tern.attention_backward(do, q, k, v, o2, lse, mask=mask)
+        check_backward(do, q, k, v, mask, None, o2, lse, got, "views")
+        assert torch.equal(o.detach(), o2)
+        assert torch.equal(qkv.grad, got[0].transpose(1, 2))
+        total = torch.cat([got[1], got[2]], 2).float().sum(0, keepdim=True)
+        assert float((kv.grad.float() - total).abs().max()) <= 2.0 ** -7 * float(total.abs().max())
+
+
+def test_backward_matches_differences():
+    # along random directions, of the function in 64 bits
+    log("attention differences")
+    b, sq, sk, hq, hkv, d = 2, 40, 50, 4, 2, 32
+    q, k, v, m = make(b, sq, sk, hq, hkv, d, "random", seed=9, spread=1.0)
+    g = torch.Generator().manual_seed(10)
+    do = torch.randn(q.shape, generator=g).to(torch.bfloat16).to(DEV)
+    o, lse = tern.attention(q, k, v, mask=m)
+    grads = tern.attention_backward(do, q, k, v, o, lse, mask=m)
+
+    def f(t):
+        s = (group(t[0], hkv) @ group(t[1], hkv).transpose(-1, -2)) / math.sqrt(d)
+        s = s.masked_fill(~m[:, None, None, None, :], -math.inf)
+        return float((ungroup(probabilities(s) @ group(t[2], hkv)) * do.double()).sum())
+
+    base = [q.double(), k.double(), v.double()]
+    for i, x in enumerate(base):
+        w = torch.randn(x.shape, generator=g).to(DEV).double()
+        up, down = list(base), list(base)
+        up[i], down[i] = x + 1e-5 * w, x - 1e-5 * w
+        diff = (f(up) - f(down)) / 2e-5
+        along = float((grads[i].double() * w).sum())
+        # every element of a gradient is a sum of independently rounded terms: the
+        # whole is within 2^-6 of its 2-norm times the direction's
+        room = 2.0 ** -6 * float(grads[i].double().norm() * w.norm()) / math.sqrt(x.numel()) * 8
+        assert abs(diff - along) <= room, (i, diff, along)
+
+
+def test_backward_without_keys_or_queries_and_refusals():
+    q, k, v, _ = make(2, 5, 4, 2, 2, 64, None, seed=1)
+    o, lse = tern.attention(q, k[:, :0], v[:, :0])
+    dq, dk, dv = tern.attention_backward(q, q, k[:, :0], v[:, :0], o, lse)
+    assert float(dq.float().abs().sum()) == 0 and dk.shape == (2, 0, 2, 64)
+    o, lse = tern.attention(q[:, :0], k, v)
+    dq, dk, dv = tern.attention_backward(q[:, :0], q[:, :0], k, v, o, lse)
+    assert dq.shape == (2, 0, 2, 64)
+    assert float(dk.float().abs().sum()) == 0 and float(dv.float().abs().sum()) == 0
+    o, lse = tern.attention(q, k, v)
+    with pytest.raises(ValueError):
+        tern.attention_backward(q, q, k, v, o, lse[:, :, :4])
+    with pytest.raises(ValueError):
+        tern.attention_backward(q[:, :4], q, k, v, o, lse)
+    with pytest.raises(TypeError):
+        tern.attention_backward(q.float(), q, k, v, o, lse)
+    with pytest.raises(tern.TernError):
+        tern.attention_backward(q, q, k, v, o, lse, scale=-1.0)
