@@ -17,7 +17,7 @@ import struct
 import torch
 
 from . import _binding as _b
-from ._binding import _check, _lib, _mat, _stream, _vec
+from ._binding import _check, _lib, _mat, _vec
 
 TERN_ROPE_INTERLEAVED = 0
 TERN_ROPE_HALVES = 1
@@ -59,22 +59,40 @@ _NORMS = {None: TERN_NORM_NONE, "layer": TERN_NORM_LAYER, "rms": TERN_NORM_RMS}
 _TYPES = {torch.float32: _b.TERN_F32, torch.bfloat16: _b.TERN_BF16}
 
 
+# A call's cost on the host counts at the smallest sizes: the checks below look at
+# a tensor once and only spell out what is wrong where something is.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(stream, a: torch.Tensor) -> int:
+    """The HIP stream to launch on: the one given, or the current one of ``a``'s GPU."""
+    return _raw_stream(a.get_device()) if stream is None else _b._stream(stream)
+
+
 def _heads(a: torch.Tensor, name: str, dtypes) -> bytes:
     """The tern_heads of a [batch, tokens, heads, width] view."""
+    try:
+        b, t, h, d = a.shape
+        sb, st, sh, sd = a.stride()
+        fits = a.is_cuda and a.dtype in dtypes and (sd == 1 or d <= 1)
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        _refuse_heads(a, name, dtypes)
+    # The stride of an axis of one element is never used.
+    return _heads_struct(a.data_ptr(), sb if b > 1 else 0, st if t > 1 else 0, sh if h > 1 else 0)
+
+
+def _refuse_heads(a, name: str, dtypes):
     if not isinstance(a, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not a.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor, got {a.device}")
     if a.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {a.dtype}, expected one of {dtypes}")
+        raise TypeError(f"{name} has dtype {a.dtype}, expected one of {tuple(dtypes)}")
     if a.dim() != 4:
         raise ValueError(f"{name} must be [batch, tokens, heads, width]")
-    b, t, h, d = a.shape
-    sb, st, sh, sd = a.stride()
-    if sd != 1 and d > 1:
-        raise ValueError(f"{name} must have consecutive channels (unit last stride)")
-    # The stride of an axis of one element is never used.
-    return _heads_struct(a.data_ptr(), sb if b > 1 else 0, st if t > 1 else 0, sh if h > 1 else 0)
+    raise ValueError(f"{name} must have consecutive channels (unit last stride)")
 
 
 @functools.lru_cache(maxsize=64)
@@ -100,10 +118,10 @@ def rope(x: torch.Tensor, pos: torch.Tensor, axes, theta: float = 10000.0,
     xs = _heads(x, "x", _TYPES)
     b, t, h, d = x.shape
     if out is None:
-        out = torch.empty((b, t, h, d), dtype=x.dtype, device=x.device)
+        out = x.new_empty((b, t, h, d))
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have the shape and dtype of x")
-    if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype != torch.float32:
+    if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype is not torch.float32:
         raise TypeError("pos must be a GPU tensor of dtype torch.float32")
     n = len(axes)
     shape = tuple(pos.shape)
@@ -116,18 +134,27 @@ def rope(x: torch.Tensor, pos: torch.Tensor, axes, theta: float = 10000.0,
     _check("tern_rope", _lib.tern_rope(xs, _heads(out, "out", _TYPES), _TYPES[x.dtype], b, t, h, d,
                                        pos.data_ptr(), pos_batch, pos_token,
                                        _axes(axes, float(theta), layout), 1 if inverse else 0,
-                                       _stream(stream)))
+                                       _stream(stream, x)))
     return out
 
 
-def _row_vectors(a, name: str, samples: int, c: int):
-    """(pointer, pitch) of a [samples, c] fp32 matrix or None."""
+_F32, _BF16 = (torch.float32,), (torch.bfloat16,)
+
+
+def _rows(a, name: str, dtypes, m: int, c: int):
+    """(pointer, pitch) of an [m, c] matrix, or of none."""
     if a is None:
-        return 0, 0
-    ld = _mat(a, name, (torch.float32,))
-    if a.shape[0] != samples or a.shape[1] != c:
-        raise ValueError(f"{name} must be [{samples}, {c}] (one row per sample)")
-    return a.data_ptr(), max(ld, c)
+        return None, 0
+    try:
+        ld, unit = a.stride()
+        fits = a.is_cuda and a.dtype in dtypes and a.shape == (m, c) and (unit == 1 or c == 1)
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        _mat(a, name, dtypes)
+        raise ValueError(f"{name} must be [{m}, {c}], got {list(a.shape)}")
+    # With a single row the pitch is never used; report one that keeps rows aligned.
+    return a.data_ptr(), ld if m > 1 else (c + 15) // 16 * 16
 
 
 def _weight(a, name: str, c: int) -> int:
@@ -147,22 +174,21 @@ def _norm_args(m, c, dtype, tokens, pre, post, eps, residual_scale, pre_weight, 
     if tokens < 1:
         raise ValueError("tokens must be at least 1")
     samples = -(-m // tokens)
+    gp, ldgate = _rows(gate, "gate", _F32, samples, c)
+    sp, ldscale = _rows(scale, "scale", _F32, samples, c)
+    hp, ldshift = _rows(shift, "shift", _F32, samples, c)
     return _norm_struct(m, c, tokens, _TYPES[dtype], _NORMS[pre], _NORMS[post], eps, residual_scale,
                         _weight(pre_weight, "pre_weight", c),
-                        _weight(post_weight, "post_weight", c),
-                        *_row_vectors(gate, "gate", samples, c),
-                        *_row_vectors(scale, "scale", samples, c),
-                        *_row_vectors(shift, "shift", samples, c)), samples
+                        _weight(post_weight, "post_weight", c), gp or 0, ldgate, sp or 0, ldscale,
+                        hp or 0, ldshift), samples
 
 
-def _rows(a, name: str, dtypes, shape):
-    """(pointer, pitch) of an [m, c] matrix or None."""
-    if a is None:
-        return 0, 0
-    ld = _mat(a, name, dtypes)
-    if a.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(a.shape)}")
-    return a.data_ptr(), ld
+def _stream_matrix(a, name: str):
+    """(pointer, pitch, rows, channels) of the residual stream's matrix."""
+    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+        _mat(a, name, _TYPES)
+    m, c = a.shape
+    return (*_rows(a, name, _TYPES, m, c), m, c)
 
 
 def residual_norm(r: torch.Tensor, y: torch.Tensor | None = None, *, gate=None, scale=None,
@@ -180,17 +206,16 @@ def residual_norm(r: torch.Tensor, y: torch.Tensor | None = None, *, gate=None, 
     one sample), the weights fp32 [c]; ``pre`` and ``post`` "layer", "rms" or
     None (``pre`` None: no ``h``).  Returns ``(r_out, h)`` with ``h`` bf16, and
     with ``with_stats`` the fp32 [m, 4] statistics for the backward pass."""
-    ldr = _mat(r, "r", _TYPES)
-    m, c = r.shape
+    rp, ldr, m, c = _stream_matrix(r, "r")
     args, _ = _norm_args(m, c, r.dtype, tokens, pre, post, eps, residual_scale, pre_weight,
                          post_weight, gate, scale, shift)
-    yp, ldy = _rows(y, "y", (torch.bfloat16,), r.shape)
-    r_out = r if y is None else torch.empty((m, c), dtype=r.dtype, device=r.device)
-    h = None if pre is None else torch.empty((m, c), dtype=torch.bfloat16, device=r.device)
-    stats = torch.empty((m, 4), dtype=torch.float32, device=r.device) if with_stats else None
+    yp, ldy = _rows(y, "y", _BF16, m, c)
+    r_out = r if y is None else r.new_empty((m, c))
+    h = None if pre is None else r.new_empty((m, c), dtype=torch.bfloat16)
+    stats = r.new_empty((m, 4), dtype=torch.float32) if with_stats else None
     _check("tern_residual_norm", _lib.tern_residual_norm(
-        args, r.data_ptr(), ldr, yp, ldy, r_out.data_ptr(), c, None if h is None else h.data_ptr(),
-        c, None if stats is None else stats.data_ptr(), _stream(stream)))
+        args, rp, ldr, yp, ldy, r_out.data_ptr(), c, None if h is None else h.data_ptr(), c,
+        None if stats is None else stats.data_ptr(), _stream(stream, r)))
     return (r_out, h, stats) if with_stats else (r_out, h)
 
 
@@ -204,41 +229,38 @@ def residual_norm_backward(dr_out, dh, r_out: torch.Tensor, y, stats: torch.Tens
     ``dh`` (bf16, or None), the stored ``r_out`` (``r`` where ``y`` was None), ``y`` and ``stats``.
     None stands for the gradient of what is not there (``dshift`` without
     ``with_shift``)."""
-    ldro = _mat(r_out, "r_out", _TYPES)
-    m, c = r_out.shape
-    shape, dtype, device = r_out.shape, r_out.dtype, r_out.device
+    rp, ldro, m, c = _stream_matrix(r_out, "r_out")
+    dtype = r_out.dtype
     args, samples = _norm_args(m, c, dtype, tokens, pre, post, eps, residual_scale, pre_weight,
                                post_weight, gate, scale, None)
-    drop, lddro = _rows(dr_out, "dr_out", (dtype,), shape)
-    dhp, lddh = _rows(dh, "dh", (torch.bfloat16,), shape)
-    yp, ldy = _rows(y, "y", (torch.bfloat16,), shape)
-    if _mat(stats, "stats", (torch.float32,)) != 4 and m > 1 or tuple(stats.shape) != (m, 4):
+    drop, lddro = _rows(dr_out, "dr_out", (dtype,), m, c)
+    dhp, lddh = _rows(dh, "dh", _BF16, m, c)
+    yp, ldy = _rows(y, "y", _BF16, m, c)
+    sp, lds = _rows(stats, "stats", _F32, m, 4)
+    if lds != 4 and m > 1:
         raise ValueError(f"stats must be a contiguous [{m}, 4] tensor")
-    dr = torch.empty((m, c), dtype=dtype, device=device)
-    dy = None if y is None else torch.empty((m, c), dtype=torch.bfloat16, device=device)
+    dr = r_out.new_empty((m, c))
+    dy = None if y is None else r_out.new_empty((m, c), dtype=torch.bfloat16)
 
     def sums(wanted, *size):
-        return torch.empty(size, dtype=torch.float32, device=device) if wanted else None
+        """One tensor for each of `wanted` (None for those that are not), and their addresses."""
+        n = sum(wanted)
+        made = iter(r_out.new_empty((n, *size), dtype=torch.float32).unbind(0) if n else ())
+        out = [next(made) if w else None for w in wanted]
+        return out + [None if a is None else a.data_ptr() for a in out]
 
-    dgate = sums(gate is not None and y is not None, samples, c)
-    dscale = sums(scale is not None and dh is not None, samples, c)
-    dshift = sums(with_shift and dh is not None, samples, c)
-    dpre = sums(pre_weight is not None and dh is not None, c)
-    dpost = sums(post_weight is not None and y is not None, c)
+    with_y, with_h = y is not None, dh is not None
+    dgate, dscale, dshift, gp, scp, shp = sums(
+        (gate is not None and with_y, scale is not None and with_h, with_shift and with_h), samples, c)
+    dpre, dpost, prp, pop = sums(
+        (pre_weight is not None and with_h, post_weight is not None and with_y), c)
     need = _lib.tern_residual_norm_bwd_workspace(args)
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-
-    def ptr(a):
-        return None if a is None else a.data_ptr()
-
+    workspace = r_out.new_empty(need, dtype=torch.uint8)
     _check("tern_residual_norm_bwd", _lib.tern_residual_norm_bwd(
-        args, drop, lddro, dhp, lddh, r_out.data_ptr(), ldro, yp, ldy, stats.data_ptr(),
-        dr.data_ptr(), c, ptr(dy), c, ptr(dgate), ptr(dscale), ptr(dshift), ptr(dpre), ptr(dpost),
-        workspace.data_ptr(), need, _stream(stream)))
+        args, drop, lddro, dhp, lddh, rp, ldro, yp, ldy, sp, dr.data_ptr(), c,
+        None if dy is None else dy.data_ptr(), c, gp, scp, shp, prp, pop, workspace.data_ptr(), need,
+        _stream(stream, r_out)))
     return dr, dy, dgate, dscale, dshift, dpre, dpost
-
-
-_BF16 = (torch.bfloat16,)
 
 
 def _attention_shape(q, k, v, scale) -> bytes:
@@ -275,13 +297,13 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask=None,
     b, s, h, d = q.shape
     shape = _attention_shape(q, k, v, scale)
     mp, ldmask = _key_mask(mask, b, k.shape[1])
-    o = torch.empty((b, s, h, d), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((b, h, s), dtype=torch.float32, device=q.device)
+    o = q.new_empty((b, s, h, d))
+    lse = q.new_empty((b, h, s), dtype=torch.float32)
     need = _lib.tern_attention_workspace(shape, mp is not None, 0)
-    workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     _check("tern_attention", _lib.tern_attention(
         qs, ks, vs, _heads(o, "o", _BF16), shape, mp, ldmask, lse.data_ptr(),
-        workspace.data_ptr() if need else None, need, _stream(stream)))
+        workspace.data_ptr() if need else None, need, _stream(stream, q)))
     return o, lse
 
 
@@ -300,10 +322,10 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     if tuple(lse.shape) != (b, h, s) or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous [{b}, {h}, {s}] tensor")
     mp, ldmask = _key_mask(mask, b, k.shape[1])
-    dq, dk, dv = (torch.empty(a.shape, dtype=torch.bfloat16, device=q.device) for a in (q, k, v))
+    dq, dk, dv = (a.new_empty(a.shape) for a in (q, k, v))
     need = _lib.tern_attention_workspace(shape, mp is not None, 1)
-    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = q.new_empty(need, dtype=torch.uint8)
     _check("tern_attention_bwd", _lib.tern_attention_bwd(
         *views, lse.data_ptr(), *(_heads(a, "gradient", _BF16) for a in (dq, dk, dv)), shape, mp,
-        ldmask, workspace.data_ptr(), need, _stream(stream)))
+        ldmask, workspace.data_ptr(), need, _stream(stream, q)))
     return dq, dk, dv

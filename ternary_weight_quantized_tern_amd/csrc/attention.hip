@@ -93,16 +93,11 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
   kcopy.plan(wave, lane, p.kt, p.d);
   vcopy.plan(wave, lane, p.vt, p.d);
 
-  uint32_t koff[DS], voffa[DT], voffb[DT];
   const uint32_t first_key = kw * (32 * kSub);  // of this wave, in a tile
-#pragma unroll
-  for (int s = 0; s < DS; ++s) koff[s] = tile_offset<CPR>(first_key + i, 2 * s + h);
-#pragma unroll
-  for (int t = 0; t < DT; ++t) {
-    transposed_offsets<CPR>(lane, t, voffa[t], voffb[t]);
-    voffa[t] += first_key * (CPR * 16u);
-    voffb[t] += first_key * (CPR * 16u);
-  }
+  RowReads<CPR> by_row;
+  by_row.plan(first_key, i, h);
+  TransposedReads<CPR> turned;
+  turned.plan(first_key, lane);
 
   auto word_of = [&](int t, int w) -> unsigned long long {
     if (MASK) return uniform64(words[(t - t_first) * kWords + w]);
@@ -141,6 +136,8 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
   float m = -INFINITY, l = 0.0f;
 
   auto compute = [&](int t, const uint8_t* kl, const uint8_t* vl) {
+    by_row.pin();
+    turned.pin();
     f32x16_t s[kSub];
 #pragma unroll
     for (int u = 0; u < kSub; ++u) s[u] = f32x16_t{};
@@ -148,7 +145,9 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
     for (int c = 0; c < DS; ++c)
 #pragma unroll
       for (int u = 0; u < kSub; ++u)
-        s[u] = mfma32(read_rows(kl, koff[c] + u * (32 * CPR * 16u)), qf[c], s[u]);
+        s[u] = mfma32(read_rows(kl + u * (32 * CPR * 16u), by_row.at(c)), qf[c], s[u]);
+    order_reads_ahead<DS, kSub, kSub, 2>();
+    phase_end();
 
     // Masked keys: S = -inf.
 #pragma unroll
@@ -158,8 +157,10 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
       if (part != 0xFFFFFFFFu) {
         const uint32_t mine = part >> (4 * h);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          s[u][e] = (mine >> ((e & 3) + 8 * (e >> 2))) & 1u ? s[u][e] : -INFINITY;
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t keep = spread_bit(mine, (e & 3) + 8 * (e >> 2));
+          s[u][e] = __uint_as_float((__float_as_uint(s[u][e]) & keep) | (0xFF800000u & ~keep));
+        }
       }
     }
     float top = s[0][0];
@@ -197,9 +198,7 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
     for (int c = 0; c < 2 * kSub; ++c)
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        o[d] = mfma32(read_transposed(vl, voffa[d] + c * (16 * CPR * 16u),
-                                      voffb[d] + c * (16 * CPR * 16u)),
-                      pf[c], o[d]);
+        o[d] = mfma32(turned.read(vl, d, c), pf[c], o[d]);
   };
 
   // Two tiles in LDS: while one is used the next is on its way.

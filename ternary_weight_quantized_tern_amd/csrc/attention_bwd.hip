@@ -21,11 +21,13 @@
 // fp32 sums a last kernel adds in order.
 // P and dS are rounded to bf16 as operands; S, dP, delta and all sums are fp32.
 #include "attention_common.h"
+#include <stdlib.h>
 
 namespace tern {
 namespace {
 
 [[maybe_unused]] constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRowTile = 32;  // rows of a tile of the kernel by keys
 
 // Column i of a transposed accumulator (channels down, as 32 dt + (e & 3) + 8 (e >> 2)
 // + 4 h) times `factor`: eight consecutive channels a lane after the halves trade.
@@ -140,11 +142,10 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
   TileCopy<CPR, BK, NW> kcopy, vcopy;
   kcopy.plan(wave, lane, p.kt, p.d);
   vcopy.plan(wave, lane, p.vt, p.d);
-  uint32_t roff[DS], toffa[DT], toffb[DT];
-#pragma unroll
-  for (int s = 0; s < DS; ++s) roff[s] = tile_offset<CPR>(i, 2 * s + h);
-#pragma unroll
-  for (int t = 0; t < DT; ++t) transposed_offsets<CPR>(lane, t, toffa[t], toffb[t]);
+  RowReads<CPR> by_row;
+  by_row.plan(0, i, h);
+  TransposedReads<CPR> turned;
+  turned.plan(0, lane);
 
   auto word_of = [&](int t) -> unsigned long long {
     if (MASK) return uniform64(words[t - t_first]);
@@ -168,14 +169,18 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
 
   auto compute = [&](int t, const uint8_t* kl, const uint8_t* vl) {
     const unsigned long long w = word_of(t);
+    by_row.pin();
+    turned.pin();
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f32x16_t s = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
       for (int c = 0; c < DS; ++c) {
-        s = mfma32(read_rows(kl, roff[c] + u * (32 * CPR * 16u)), qf[c], s);
-        dp = mfma32(read_rows(vl, roff[c] + u * (32 * CPR * 16u)), dof[c], dp);
+        s = mfma32(read_rows(kl + u * (32 * CPR * 16u), by_row.at(c)), qf[c], s);
+        dp = mfma32(read_rows(vl + u * (32 * CPR * 16u), by_row.at(c)), dof[c], dp);
       }
+      order_reads_ahead<DS, 2, 2, 2>();
+      phase_end();
       const uint32_t part = static_cast<uint32_t>(w >> (32 * u));
       float x[16];
 #pragma unroll
@@ -185,16 +190,15 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
         const uint32_t mine = part >> (4 * h);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          x[e] = (mine >> ((e & 3) + 8 * (e >> 2))) & 1u ? x[e] : 0.0f;
+          x[e] = __uint_as_float(__float_as_uint(x[e]) &
+                                 spread_bit(mine, (e & 3) + 8 * (e >> 2)));
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const bf16x8_t ds = to_operand(x + 8 * c);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
-          dq[d] = mfma32(read_transposed(kl, toffa[d] + (2 * u + c) * (16 * CPR * 16u),
-                                         toffb[d] + (2 * u + c) * (16 * CPR * 16u)),
-                         ds, dq[d]);
+          dq[d] = mfma32(turned.read(kl, d, 2 * u + c), ds, dq[d]);
       }
     }
   };
@@ -230,18 +234,19 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
 }
 
 template <int CPR, bool MASK>
-__global__ __launch_bounds__(256, CPR > 10 ? 1 : 2) void attention_dkv_kernel(
-    AttentionBwdParams p) {
+__global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttentionBwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int NW = 4, BR = 64, DS = CPR / 2, DT = (CPR + 3) / 4;
+  constexpr int NW = 4, BR = kRowTile, BK = 32 * NW, DS = CPR / 2, DT = (CPR + 3) / 4;
+  constexpr bool kValuesInLds = CPR > 10;
   constexpr uint32_t kBytes = tile_bytes<CPR>(BR);
   __shared__ __attribute__((aligned(1024))) uint8_t q0[kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t q1[kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t o0[kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t o1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t values[kValuesInLds ? tile_bytes<CPR>(BK) : 16];
   // lse2 and delta of a tile's rows.
-  __shared__ __attribute__((aligned(1024))) float st0[2 * BR];
-  __shared__ __attribute__((aligned(1024))) float st1[2 * BR];
+  __shared__ __attribute__((aligned(1024))) float st0[2 * 64];
+  __shared__ __attribute__((aligned(1024))) float st1[2 * 64];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -254,52 +259,66 @@ __global__ __launch_bounds__(256, CPR > 10 ? 1 : 2) void attention_dkv_kernel(
   const uint32_t bh = at / p.dkv_splits;
   const int hk = bh % p.hkv, b = bh / p.hkv;
 
-  const int64_t key = (static_cast<int64_t>(block) * NW + wave) * 32 + i;
+  const int64_t first_key = static_cast<int64_t>(block) * BK;
+  const int64_t key = first_key + 32 * wave + i;
   const bool in = key < p.sk;
   int t_first = split * p.row_tiles_per_split;
   int t_end = t_first + p.row_tiles_per_split < p.row_tiles ? t_first + p.row_tiles_per_split
                                                             : p.row_tiles;
-  bool kept = in;
-  if (MASK) {
-    const uint8_t* mask = p.mask + b * p.ldmask;
-    kept = in && mask[key] != 0;
-    const int64_t first = static_cast<int64_t>(block) * (32 * NW);
-    const bool any = (first + lane < p.sk && mask[first + lane] != 0) ||
-                     (first + 64 + lane < p.sk && mask[first + 64 + lane] != 0);
-    if (__ballot(any) == 0) t_end = t_first;  // the same in every wave: nothing to add
+  unsigned long long words[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if (MASK) {
+      const int64_t s = first_key + 64 * w + lane;
+      words[w] = __ballot(s < p.sk && p.mask[b * p.ldmask + s] != 0);
+    } else {
+      words[w] = tail_word(first_key + 64 * w, p.sk);
+    }
   }
+  if ((words[0] | words[1]) == 0) t_end = t_first;  // the same in every wave: nothing to add
+  const bool kept = ((words[wave >> 1] >> ((32 * wave + i) & 63)) & 1ull) != 0;
 
-  // The keys and values of this lane's column (zeros where they do not count).
-  bf16x8_t kf[DS], vf[DS];
+  // The keys (and, where registers allow, values) of this lane's column; zeros
+  // where they do not count.
+  bf16x8_t kf[DS], vf[kValuesInLds ? 1 : DS];
   {
     const uint16_t* k = p.k + b * p.kb + hk * p.kh + key * p.kt;
     const uint16_t* v = p.v + b * p.vb + hk * p.vh + key * p.vt;
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
       const int c = 16 * s + 8 * h;
-      kf[s] = vf[s] = bf16x8_t{};
-      if (kept && c < p.d) {
-        kf[s] = *reinterpret_cast<const bf16x8_t*>(k + c);
-        vf[s] = *reinterpret_cast<const bf16x8_t*>(v + c);
+      kf[s] = bf16x8_t{};
+      if (kept && c < p.d) kf[s] = *reinterpret_cast<const bf16x8_t*>(k + c);
+      if constexpr (!kValuesInLds) {
+        vf[s] = bf16x8_t{};
+        if (kept && c < p.d) vf[s] = *reinterpret_cast<const bf16x8_t*>(v + c);
       }
+    }
+  }
+  if constexpr (kValuesInLds) {
+    if (t_first < t_end) {
+      TileCopy<CPR, BK, NW> vcopy;
+      vcopy.plan(wave, lane, p.vt, p.d);
+      auto keep = [&](uint32_t r) { return ((words[r >> 6] >> (r & 63u)) & 1ull) != 0; };
+      vcopy.issue(p.v + b * p.vb + hk * p.vh + first_key * p.vt, values, wave, lane,
+                  (words[0] & words[1]) == ~0ull, keep);
     }
   }
 
   TileCopy<CPR, BR, NW> qcopy, ocopy;
   qcopy.plan(wave, lane, p.qt, p.d);
   ocopy.plan(wave, lane, p.dot, p.d);
-  uint32_t roff[DS], toffa[DT], toffb[DT];
-#pragma unroll
-  for (int s = 0; s < DS; ++s) roff[s] = tile_offset<CPR>(i, 2 * s + h);
-#pragma unroll
-  for (int t = 0; t < DT; ++t) transposed_offsets<CPR>(lane, t, toffa[t], toffb[t]);
+  RowReads<CPR> by_row;
+  by_row.plan(0, i, h);
+  TransposedReads<CPR> turned;
+  turned.plan(0, lane);
 
-  // Row tile t: head t / tiles_per_head of the group, 64 tokens.
+  // Row tile t: head t / tiles_per_head of the group, BR tokens.
   auto issue = [&](int t, uint8_t* ql, uint8_t* ol, float* st) {
-    const int g = t / p.tiles_per_head;
-    const int64_t token = static_cast<int64_t>(t - g * p.tiles_per_head) * BR;
+    const int g = t < t_end ? t / p.tiles_per_head : 0;
+    const int64_t token = t < t_end ? static_cast<int64_t>(t - g * p.tiles_per_head) * BR : 0;
     const int head = hk * p.group + g;
-    const int left = p.sq - static_cast<int>(token);
+    const int left = t < t_end ? p.sq - static_cast<int>(token) : 0;
     auto keep = [&](uint32_t r) { return static_cast<int>(r) < left; };
     qcopy.issue(p.q + b * p.qb + head * p.qh + token * p.qt, ql, wave, lane, left >= BR, keep);
     ocopy.issue(p.dout + b * p.dob + head * p.doh + token * p.dot, ol, wave, lane, left >= BR,
@@ -308,7 +327,7 @@ __global__ __launch_bounds__(256, CPR > 10 ? 1 : 2) void attention_dkv_kernel(
       const float* src = (wave == 0 ? p.lse2 : p.delta) +
                          (static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + token;
       const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(src, 4u * (left < BR ? left : BR));
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)(st + wave * BR), 4, 4 * lane, 0,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)(st + wave * 64), 4, 4 * lane, 0,
                                                0, 0);
     }
   };
@@ -318,19 +337,25 @@ __global__ __launch_bounds__(256, CPR > 10 ? 1 : 2) void attention_dkv_kernel(
   for (int t = 0; t < DT; ++t) dk[t] = dv[t] = f32x16_t{};
 
   auto compute = [&](const uint8_t* ql, const uint8_t* ol, const float* st) {
+    by_row.pin();
+    turned.pin();
 #pragma unroll
     for (int u = 0; u < BR / 32; ++u) {
       f32x16_t s = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
       for (int c = 0; c < DS; ++c) {
-        s = mfma32(read_rows(ql, roff[c] + u * (32 * CPR * 16u)), kf[c], s);
-        dp = mfma32(read_rows(ol, roff[c] + u * (32 * CPR * 16u)), vf[c], dp);
+        s = mfma32(read_rows(ql + u * (32 * CPR * 16u), by_row.at(c)), kf[c], s);
+        const bf16x8_t v = kValuesInLds ? read_rows(values + wave * (32 * CPR * 16u), by_row.at(c))
+                                        : vf[kValuesInLds ? 0 : c];
+        dp = mfma32(read_rows(ol + u * (32 * CPR * 16u), by_row.at(c)), v, dp);
       }
+      order_reads_ahead<DS, 2, kValuesInLds ? 3 : 2, 2>();
+      phase_end();
       float x[16], y[16];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4_t lse2 = *reinterpret_cast<const f32x4_t*>(st + 32 * u + 8 * g + 4 * h);
-        const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(st + BR + 32 * u + 8 * g + 4 * h);
+        const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(st + 64 + 32 * u + 8 * g + 4 * h);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * g + e;
@@ -343,28 +368,28 @@ __global__ __launch_bounds__(256, CPR > 10 ? 1 : 2) void attention_dkv_kernel(
         const bf16x8_t pf = to_operand(x + 8 * c), df = to_operand(y + 8 * c);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const uint32_t a = toffa[d] + (2 * u + c) * (16 * CPR * 16u);
-          const uint32_t q = toffb[d] + (2 * u + c) * (16 * CPR * 16u);
-          dv[d] = mfma32(read_transposed(ol, a, q), pf, dv[d]);
-          dk[d] = mfma32(read_transposed(ql, a, q), df, dk[d]);
+          dv[d] = mfma32(turned.read(ol, d, 2 * u + c), pf, dv[d]);
+          dk[d] = mfma32(turned.read(ql, d, 2 * u + c), df, dk[d]);
         }
       }
     }
   };
 
-  int t = t_first;
-  if (t < t_end) issue(t, q0, o0, st0);
-  while (t < t_end) {
-    wait_vmem();
-    tile_barrier();
-    if (t + 1 < t_end) issue(t + 1, q1, o1, st1);
-    compute(q0, o0, st0);
-    if (++t >= t_end) break;
-    wait_vmem();
-    tile_barrier();
-    if (t + 1 < t_end) issue(t + 1, q0, o0, st0);
-    compute(q1, o1, st1);
-    ++t;
+  // Tiles in pairs, so that the loop has one exit and the accumulators stay where
+  // they are; a tile past the end arrives as zeros and adds nothing.
+  if (t_first < t_end) {
+    issue(t_first, q0, o0, st0);
+    for (int t = t_first; t < t_end; t += 2) {
+      wait_vmem();
+      tile_barrier();
+      issue(t + 1, q1, o1, st1);
+      compute(q0, o0, st0);
+      wait_vmem();
+      tile_barrier();
+      issue(t + 2, q0, o0, st0);
+      compute(q1, o1, st1);
+    }
+    wait_vmem();  // no copy may outlive the workgroup's LDS
   }
 
   if (!kept) {
@@ -438,9 +463,9 @@ BwdPlan plan(const AttentionBwdParams& p) {
   split(r.key_tiles, bh * r.row_blocks, 512, 4, p.mask ? kMaskWords : int64_t(1) << 30,
         &r.key_tiles_per_split, &r.dq_splits);
   r.key_blocks = static_cast<int>((p.sk + 127) / 128);
-  r.tiles_per_head = (p.sq + 63) / 64;
+  r.tiles_per_head = (p.sq + kRowTile - 1) / kRowTile;
   r.row_tiles = r.tiles_per_head * p.group;
-  split(r.row_tiles, bh * r.key_blocks, p.d > 80 ? 256 : 512, 4, int64_t(1) << 30,
+  split(r.row_tiles, bh * r.key_blocks, getenv("WANT") ? atoi(getenv("WANT")) : 512, 8, int64_t(1) << 30,
         &r.row_tiles_per_split, &r.dkv_splits);
   auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
   r.stats = whole(bh * p.rows);

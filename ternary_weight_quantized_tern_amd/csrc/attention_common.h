@@ -120,15 +120,65 @@ __device__ inline bf16x8_t read_transposed(const uint8_t* lds, uint32_t a, uint3
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// Offsets of a lane's transposing reads of 32-channel group dt, rows 0 .. 15 of a
-// tile (16 rows on: 16 CPR * 16 bytes more; the swizzle repeats every 16 rows).
+// Where lane (i, h) finds its operands in a tile, from few registers: the swizzle acts on
+// low bits, so the offset of another step or channel group differs by an exclusive or with
+// (or the addition of) a constant.  pin() keeps the compiler from precomputing
+// them all into registers outside a loop.
 template <int CPR>
-__device__ inline void transposed_offsets(int lane, int dt, uint32_t& a, uint32_t& b) {
-  const uint32_t h = lane >> 5, g = (lane >> 4) & 1, j = (lane >> 2) & 3, k = lane & 3;
-  const uint32_t chunk = 4u * dt + 2u * g + (k >> 1), sub = (k & 1u) * 8u;
-  a = tile_offset<CPR>(4u * h + j, chunk) + sub;
-  b = tile_offset<CPR>(4u * h + j + 8u, chunk) + sub;
+struct RowReads {
+  uint32_t base;
+  __device__ void plan(int first, int i, int h) { base = tile_offset<CPR>(first + i, h); }
+  __device__ void pin() { asm volatile("" : "+v"(base)); }
+  // Channels 16 c + 8 h .. + 7 of the lane's row.
+  __device__ uint32_t at(int c) const {
+    if constexpr (CPR == 16 || CPR == 8)
+      return base ^ (32u * c);
+    else if constexpr (CPR == 10)
+      return base + 32u * c;
+    else
+      return (base ^ (32u * (c & 1))) + 64u * (c >> 1);
+  }
+};
+
+// Transposing reads of rows 0 .. 15 (16 rows on: 16 CPR * 16 bytes more; the
+// swizzle repeats every 16 rows).
+template <int CPR>
+struct TransposedReads {
+  uint32_t a, b;
+  __device__ void plan(int first, int lane) {
+    const uint32_t h = lane >> 5, g = (lane >> 4) & 1, j = (lane >> 2) & 3, k = lane & 3;
+    const uint32_t chunk = 2u * g + (k >> 1), sub = (k & 1u) * 8u;
+    a = tile_offset<CPR>(first + 4u * h + j, chunk) + sub;
+    b = tile_offset<CPR>(first + 4u * h + j + 8u, chunk) + sub;
+  }
+  __device__ void pin() {
+    asm volatile("" : "+v"(a));
+    asm volatile("" : "+v"(b));
+  }
+  // Channels 32 dt .. + 31 of rows 16 r .. + 15.
+  __device__ bf16x8_t read(const uint8_t* lds, int dt, int r) const {
+    const uint32_t rows = r * (16 * CPR * 16u);
+    if constexpr (CPR == 16 || CPR == 8)
+      return read_transposed(lds + rows, a ^ (64u * dt), b ^ (64u * dt));
+    else
+      return read_transposed(lds + rows, a + 64u * dt, b + 64u * dt);
+  }
+};
+
+// Order of a stretch of `products` MFMAs whose operands take `reads` LDS reads each
+// `step` of them: the reads run `ahead` steps in front of the products. Left
+// alone, the compiler places each read right before its product to save
+// registers, and every product waits out the LDS latency.
+template <int STEPS, int PRODUCTS, int READS, int AHEAD>
+__device__ inline void order_reads_ahead() {
+  constexpr int kMfma = 0x008, kDsRead = 0x100;
+#pragma unroll
+  for (int s = 0; s < STEPS + AHEAD; ++s) {
+    if (s >= AHEAD) __builtin_amdgcn_sched_group_barrier(kMfma, PRODUCTS, 0);
+    if (s < STEPS) __builtin_amdgcn_sched_group_barrier(kDsRead, READS, 0);
+  }
 }
+__device__ inline void phase_end() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ inline f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -182,6 +232,11 @@ __device__ inline unsigned long long uniform64(unsigned long long v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
   const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
   return (static_cast<unsigned long long>(hi) << 32) | lo;
+}
+
+// All ones where bit `bit` is set, else 0.
+__device__ inline uint32_t spread_bit(uint32_t bits, int bit) {
+  return static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(bits), bit, 1));
 }
 
 // Bits of the keys below `keys` among 64 from key0 on.
