@@ -66,12 +66,6 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
 
   const int t_first = split * p.tiles_per_split;
   const int t_end = t_first + p.tiles_per_split < p.tiles ? t_first + p.tiles_per_split : p.tiles;
-  if (MASK) {
-    mask_words(words, p.mask + b * p.ldmask, static_cast<int64_t>(t_first) * BK, p.sk,
-               (t_end - t_first) * kWords, wave, NW, lane);
-    __syncthreads();
-  }
-
   // The rows of this lane's column, as the B operand of S^T.
   const int row = (block * RW + rw) * 32 + i;
   const PackedRow pr = packed_row(row, p.rows, p.sq);
@@ -85,6 +79,12 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
       qf[s] = bf16x8_t{};
       if (pr.live && c < p.d) qf[s] = *reinterpret_cast<const bf16x8_t*>(q + c);
     }
+  }
+
+  if (MASK) {
+    mask_words(words, p.mask + b * p.ldmask, static_cast<int64_t>(t_first) * BK, p.sk,
+               (t_end - t_first) * kWords, wave, NW, lane);
+    __syncthreads();
   }
 
   const uint16_t* kbase = p.k + b * p.kb + hk * p.kh;
@@ -201,23 +201,51 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
         o[d] = mfma32(turned.read(vl, d, c), pf[c], o[d]);
   };
 
-  // Two tiles in LDS: while one is used the next is on its way.
   int t = next_tile(t_first);
-  if (t < t_end) issue(t, k0, v0);
-  while (t < t_end) {
-    wait_vmem();
-    tile_barrier();
-    int n = next_tile(t + 1);
+  if constexpr (KW == 1) {
+    // Two tiles in LDS: while one is used the next is on its way.
+    if (t < t_end) issue(t, k0, v0);
+    while (t < t_end) {
+      wait_vmem();
+      tile_barrier();
+      int n = next_tile(t + 1);
+      if (n < t_end) issue(n, k1, v1);
+      compute(t, k0, v0);
+      t = n;
+      if (t >= t_end) break;
+      wait_vmem();
+      tile_barrier();
+      n = next_tile(t + 1);
+      if (n < t_end) issue(n, k0, v0);
+      compute(t, k1, v1);
+      t = n;
+    }
+  } else {
+    // A stream of keys: two tiles on their way from the start, and a buffer asked
+    // for again as soon as every wave is done with it.
+    constexpr int kTile = 2 * TileCopy<CPR, BK, NW>::kOwn;
+    static_assert(TileCopy<CPR, BK, NW>::kInstr % NW == 0, "each wave issues the same copies");
+    int n = t < t_end ? next_tile(t + 1) : t_end;
+    if (t < t_end) issue(t, k0, v0);
     if (n < t_end) issue(n, k1, v1);
-    compute(t, k0, v0);
-    t = n;
-    if (t >= t_end) break;
-    wait_vmem();
-    tile_barrier();
-    n = next_tile(t + 1);
-    if (n < t_end) issue(n, k0, v0);
-    compute(t, k1, v1);
-    t = n;
+    auto use = [&](uint8_t* kl, uint8_t* vl) {
+      // The tile after this one is the only one that may still be in flight.
+      if (n < t_end)
+        wait_vmem<kTile>();
+      else
+        wait_vmem();
+      tile_barrier();
+      compute(t, kl, vl);
+      t = n;
+      if (t >= t_end) return false;
+      n = next_tile(t + 1);
+      tile_barrier();
+      if (n < t_end) issue(n, kl, vl);
+      return true;
+    };
+    if (t < t_end)
+      while (use(k0, v0) && use(k1, v1)) {
+      }
   }
 
   {
@@ -286,16 +314,21 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
       if (j.y > 0.0f) total += j.y * __builtin_amdgcn_exp2f((j.x - top) * p.scale_log2);
     }
     const float inv = total > 0.0f ? mine / total : 0.0f;
-    // [32 rows][32 DT channels] of each wave, in the tiles' buffers.
+    // [32 rows][32 DT channels] of each wave, in the tiles' buffers; rows a bank apart.
+    constexpr int kPitch = 32 * DT + 4;
     float* parts[4] = {reinterpret_cast<float*>(k0), reinterpret_cast<float*>(k1),
                        reinterpret_cast<float*>(v0), reinterpret_cast<float*>(v1)};
-    static_assert(KW == 4 && kBytes >= 32u * 32 * DT * 4, "a wave's part fits a buffer");
+    static_assert(KW == 4 && kBytes >= 32u * kPitch * 4, "a wave's part fits a buffer");
     float* own = kw == 0 ? parts[0] : kw == 1 ? parts[1] : kw == 2 ? parts[2] : parts[3];
+    if (pr.live) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        own[i * (32 * DT) + 32 * d + (e & 3) + 8 * (e >> 2) + 4 * h] = o[d][e] * inv;
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4_t*>(own + i * kPitch + 32 * d + 8 * g + 4 * h) =
+              f32x4_t{o[d][4 * g] * inv, o[d][4 * g + 1] * inv, o[d][4 * g + 2] * inv,
+                      o[d][4 * g + 3] * inv};
+    }
     __syncthreads();
     const float lse2 =
         total > 0.0f ? __builtin_fmaf(top, p.scale_log2, __builtin_amdgcn_logf(total)) : -INFINITY;
@@ -315,7 +348,7 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
       float sum[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int off = r * (32 * DT) + c + e;
+        const int off = r * kPitch + c + e;
         sum[e] = (parts[0][off] + parts[1][off]) + (parts[2][off] + parts[3][off]);
       }
       if (p.splits > 1) {
@@ -332,44 +365,75 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-// The parts of a row, weighted by their shares of the sum: eight channels a thread.
+// The parts of a row, weighted by their shares of the sum.  A wave to a row:
+// lane (g, x), g < 4, takes every fourth part's eight channels from 8 x on, four
+// parts' loads at a time; the lanes of equal x are added at the end.
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) {
-  const int chunks = p.d / 8;
   const int64_t rows = static_cast<int64_t>(p.b) * p.hkv * p.rows;
-  const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (x >= rows * chunks) return;
-  const int64_t r = x / chunks;
-  const int c = static_cast<int>(x - r * chunks) * 8;
-  float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * rows + r]);
-  float total = 0.0f, sum[8] = {};
-  if (top > -INFINITY) {
-    for (int s = 0; s < p.splits; ++s) {
-      const float w = __builtin_amdgcn_exp2f(p.part_lse[s * rows + r] - top);
-      const float* in = p.part_o + (s * rows + r) * p.d + c;
-      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(in);
-      const f32x4_t q = *reinterpret_cast<const f32x4_t*>(in + 4);
-      total += w;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (r >= rows) return;
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = (lane & 15) * 8;
+  const bool in = c < p.d;
+  float top = -INFINITY, total = 0.0f, sum[8] = {};
+  for (int s0 = g; s0 < p.splits; s0 += 16) {
+    float lse[4];
+    f32x4_t a[4], b[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum[e] = __builtin_fmaf(w, a[e], sum[e]);
-        sum[4 + e] = __builtin_fmaf(w, q[e], sum[4 + e]);
+    for (int x = 0; x < 4; ++x) {
+      const int s = s0 + 4 * x;
+      const bool have = s < p.splits;
+      lse[x] = have ? p.part_lse[s * rows + r] : -INFINITY;
+      a[x] = b[x] = f32x4_t{};
+      if (have && in) {
+        const float* part = p.part_o + (s * rows + r) * p.d + c;
+        a[x] = *reinterpret_cast<const f32x4_t*>(part);
+        b[x] = *reinterpret_cast<const f32x4_t*>(part + 4);
       }
     }
-    const float inv = 1.0f / total;
+    const float to = fmaxf(fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])), top);
+    if (to > -INFINITY) {
+      const float old = __builtin_amdgcn_exp2f(top - to);
+      top = to;
+      total *= old;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] *= inv;
+      for (int e = 0; e < 8; ++e) sum[e] *= old;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float w = __builtin_amdgcn_exp2f(lse[x] - top);
+        total += w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[e] = __builtin_fmaf(w, a[x][e], sum[e]);
+          sum[4 + e] = __builtin_fmaf(w, b[x][e], sum[4 + e]);
+        }
+      }
+    }
+  }
+  float all = top;
+  all = fmaxf(all, __shfl_xor(all, 16));
+  all = fmaxf(all, __shfl_xor(all, 32));
+  const float mine = top > -INFINITY ? __builtin_amdgcn_exp2f(top - all) : 0.0f;
+  total *= mine;
+  total += __shfl_xor(total, 16);
+  total += __shfl_xor(total, 32);
+  const float share = total > 0.0f ? mine / total : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    sum[e] *= share;
+    sum[e] += __shfl_xor(sum[e], 16);
+    sum[e] += __shfl_xor(sum[e], 32);
   }
   const int64_t bh = r / p.rows;
   const int row = static_cast<int>(r - bh * p.rows);
   const int b = static_cast<int>(bh / p.hkv), hk = static_cast<int>(bh - static_cast<int64_t>(b) * p.hkv);
   const PackedRow to = packed_row(row, p.rows, p.sq);
   const int head = hk * p.group + to.head;
-  *reinterpret_cast<bf16x8_t*>(p.o + b * p.ob + static_cast<int64_t>(to.token) * p.ot +
-                               static_cast<int64_t>(head) * p.oh + c) = to_operand(sum);
-  if (c == 0 && p.lse != nullptr)
+  if (g == 0 && in)
+    *reinterpret_cast<bf16x8_t*>(p.o + b * p.ob + static_cast<int64_t>(to.token) * p.ot +
+                                 static_cast<int64_t>(head) * p.oh + c) = to_operand(sum);
+  if (lane == 0 && p.lse != nullptr)
     p.lse[(static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + to.token] =
-        top > -INFINITY ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+        total > 0.0f ? (all + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
 }
 
 constexpr int kFewRows = 64;
@@ -444,9 +508,9 @@ hipError_t launch_attention(AttentionParams& p, void* workspace, hipStream_t str
                        : p.d <= 96 ? launch<12>(p, r.few, grid, stream)
                                    : launch<16>(p, r.few, grid, stream);
   if (e != hipSuccess || r.splits == 1) return e;
-  const int64_t threads = rows * (p.d / 8);
-  hipLaunchKernelGGL(attention_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)),
-                     dim3(256), 0, stream, p);
+  if ((rows + 3) / 4 > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(attention_join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256),
+                     0, stream, p);
   return hipGetLastError();
 }
 

@@ -21,7 +21,6 @@
 // fp32 sums a last kernel adds in order.
 // P and dS are rounded to bf16 as operands; S, dP, delta and all sums are fp32.
 #include "attention_common.h"
-#include <stdlib.h>
 
 namespace tern {
 namespace {
@@ -94,12 +93,6 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
   const int t_first = split * p.key_tiles_per_split;
   const int t_end = t_first + p.key_tiles_per_split < p.key_tiles ? t_first + p.key_tiles_per_split
                                                                   : p.key_tiles;
-  if (MASK) {
-    mask_words(words, p.mask + b * p.ldmask, static_cast<int64_t>(t_first) * BK, p.sk,
-               t_end - t_first, wave, NW, lane);
-    __syncthreads();
-  }
-
   const int row = (block * NW + wave) * 32 + i;
   const PackedRow pr = packed_row(row, p.rows, p.sq);
   const int head = hk * p.group + pr.head;
@@ -135,6 +128,12 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
   if (pr.live && h == 0 && split == 0) {
     p.lse2[stat] = lse2;
     p.delta[stat] = delta;
+  }
+
+  if (MASK) {
+    mask_words(words, p.mask + b * p.ldmask, static_cast<int64_t>(t_first) * BK, p.sk,
+               t_end - t_first, wave, NW, lane);
+    __syncthreads();
   }
 
   const uint16_t* kbase = p.k + b * p.kb + hk * p.kh;
@@ -407,33 +406,38 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttentionBwdParam
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-// The splits' sums of one gradient, added in order: eight channels a thread.
-// rows = heads_per_kv * tokens rows of each (sample, kv head).
-__global__ __launch_bounds__(256) void attention_add_kernel(const float* part, int splits,
-                                                            uint16_t* out, int64_t ob, int64_t ot,
-                                                            int64_t oh, int hkv, int group,
-                                                            int64_t tokens, int64_t total, int d) {
-  const int chunks = d / 8;
+// The splits' sums, added in order: eight channels a thread.  Two gradients of
+// the same sizes (dk and dv) are two rows of workgroups.
+struct Sums {
+  const float* part;
+  uint16_t* out;
+  int64_t batch, token, head;  // strides of out
+};
+__global__ __launch_bounds__(256) void attention_add_kernel(Sums a, Sums b, int splits, int hkv,
+                                                            int group, int64_t tokens,
+                                                            int64_t total, int d) {
+  const Sums g = blockIdx.y ? b : a;
+  const uint32_t chunks = d / 8;
   const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (x >= total * chunks) return;
   const int64_t r = x / chunks;
   const int c = static_cast<int>(x - r * chunks) * 8;
   float sum[8] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float* in = part + (s * total + r) * d + c;
-    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(in);
-    const f32x4_t b = *reinterpret_cast<const f32x4_t*>(in + 4);
+  const float* in = g.part + r * d + c;
+  for (int s = 0; s < splits; ++s, in += total * d) {
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(in);
+    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(in + 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      sum[e] += a[e];
-      sum[4 + e] += b[e];
+      sum[e] += lo[e];
+      sum[4 + e] += hi[e];
     }
   }
-  const int64_t head = r / tokens, token = r - head * tokens;  // over sample, kv head, group
+  const int64_t row = r / tokens, token = r - row * tokens;  // over sample, kv head, group
   const int64_t heads = static_cast<int64_t>(hkv) * group;
-  const int64_t b = head / heads;
-  *reinterpret_cast<bf16x8_t*>(out + b * ob + token * ot + (head - b * heads) * oh + c) =
-      to_operand(sum);
+  const int64_t sample = row / heads;
+  *reinterpret_cast<bf16x8_t*>(g.out + sample * g.batch + token * g.token +
+                               (row - sample * heads) * g.head + c) = to_operand(sum);
 }
 
 struct BwdPlan {
@@ -465,7 +469,7 @@ BwdPlan plan(const AttentionBwdParams& p) {
   r.key_blocks = static_cast<int>((p.sk + 127) / 128);
   r.tiles_per_head = (p.sq + kRowTile - 1) / kRowTile;
   r.row_tiles = r.tiles_per_head * p.group;
-  split(r.row_tiles, bh * r.key_blocks, getenv("WANT") ? atoi(getenv("WANT")) : 512, 8, int64_t(1) << 30,
+  split(r.row_tiles, bh * r.key_blocks, 512, 8, int64_t(1) << 30,
         &r.row_tiles_per_split, &r.dkv_splits);
   auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
   r.stats = whole(bh * p.rows);
@@ -499,12 +503,12 @@ hipError_t launch(const AttentionBwdParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t add(const float* part, int splits, uint16_t* out, int64_t ob, int64_t ot, int64_t oh,
-               int hkv, int group, int64_t tokens, int64_t total, int d, hipStream_t stream) {
+hipError_t add(const Sums& a, const Sums& b, int gradients, int splits, int hkv, int group,
+               int64_t tokens, int64_t total, int d, hipStream_t stream) {
   const int64_t blocks = (total * (d / 8) + 255) / 256;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(attention_add_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                     stream, part, splits, out, ob, ot, oh, hkv, group, tokens, total, d);
+  hipLaunchKernelGGL(attention_add_kernel, dim3(static_cast<unsigned>(blocks), gradients),
+                     dim3(256), 0, stream, a, b, splits, hkv, group, tokens, total, d);
   return hipGetLastError();
 }
 
@@ -538,15 +542,14 @@ hipError_t launch_attention_bwd(AttentionBwdParams& p, void* workspace, hipStrea
                  : p.d <= 96 ? launch<12>(p, stream)
                              : launch<16>(p, stream);
   const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
-  if (e == hipSuccess && r.dq_splits > 1 && p.rows > 0)
-    e = add(p.part_dq, r.dq_splits, p.dq, p.dqb, p.dqt, p.dqh, p.hkv, p.group, p.sq, bh * p.rows,
-            p.d, stream);
+  if (e == hipSuccess && r.dq_splits > 1 && p.rows > 0) {
+    const Sums dq = {p.part_dq, p.dq, p.dqb, p.dqt, p.dqh};
+    e = add(dq, dq, 1, r.dq_splits, p.hkv, p.group, p.sq, bh * p.rows, p.d, stream);
+  }
   if (e == hipSuccess && r.dkv_splits > 1 && p.sk > 0) {
-    e = add(p.part_dk, r.dkv_splits, p.dk, p.dkb, p.dkt, p.dkh, p.hkv, 1, p.sk, bh * p.sk, p.d,
-            stream);
-    if (e == hipSuccess)
-      e = add(p.part_dv, r.dkv_splits, p.dv, p.dvb, p.dvt, p.dvh, p.hkv, 1, p.sk, bh * p.sk, p.d,
-              stream);
+    const Sums dk = {p.part_dk, p.dk, p.dkb, p.dkt, p.dkh};
+    const Sums dv = {p.part_dv, p.dv, p.dvb, p.dvt, p.dvh};
+    e = add(dk, dv, 2, r.dkv_splits, p.hkv, 1, p.sk, bh * p.sk, p.d, stream);
   }
   return e;
 }

@@ -50,8 +50,11 @@ constexpr uint32_t tile_bytes(int rows) {
   return rows * CPR * 16u + (CPR == 10 ? 64u : 0u);
 }
 
+// Until at most N of this wave's copies (they complete in order) are in flight.
+template <int N = 0>
 __device__ inline void wait_vmem() {
-  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // vmcnt(0) only
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
 // Barrier that orders LDS accesses without __syncthreads()' fence, which would also

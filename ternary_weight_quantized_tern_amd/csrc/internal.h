@@ -142,7 +142,8 @@ struct ResidualNormBwdParams {
 
   int64_t rows, samples;   // rows a workgroup walks over
   int32_t threads, slots;  // threads to a row, rows side by side
-  float *part, *totals;    // in the workspace
+  uint32_t sample_rows;    // workgroup rows that add up samples
+  float* part;             // in the workspace
 };
 int64_t residual_norm_bwd_workspace(int64_t m, int64_t c, int64_t tokens);
 hipError_t launch_residual_norm_bwd(ResidualNormBwdParams& params, bool r_is_bf16, void* workspace,

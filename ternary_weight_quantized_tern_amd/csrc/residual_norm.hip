@@ -23,9 +23,8 @@
 // Backward, the sums over rows are S = sum dh n, Z = sum dr zn and H = sum dh:
 // dscale = w_pre S, dgate = alpha w_post Z, dshift = H, and the weights'
 // gradients are sums of (1 + scale) S and alpha gate Z over samples.  A
-// workgroup writes one partial triple for each sample that it meets, a second kernel
-// adds a sample's partials in order, a third (only for weights) the samples'.
-// No atomics: the order is fixed by the sizes.
+// workgroup writes one partial triple for each sample that it meets, and a second kernel
+// adds them in order.  No atomics: the order is fixed by the sizes.
 #include "internal.h"
 #include "wave.h"
 
@@ -207,13 +206,9 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
   const int64_t row1 = row0 + p.rows < p.m ? row0 + p.rows : p.m;
   const bool has_y = p.y != nullptr, has_h = p.h != nullptr;
 
-  float gate[NCH][8], scale[NCH][8], shift[NCH][8], wpre[NCH][8], wpost[NCH][8];
-#pragma unroll
-  for (int j = 0; j < NCH; ++j) {
-    load_vector<WIDE>(p.pre_weight, wpre[j], 1.0f, j, n, lane, c);
-    load_vector<WIDE>(p.post_weight, wpost[j], 1.0f, j, n, lane, c);
-  }
-  int64_t sample = -1, sample_end = 0;
+  // Of the row's sample: alpha gate w_post, w_pre (1 + scale), shift.
+  float gate[NCH][8], scale[NCH][8], shift[NCH][8];
+  int64_t sample_end = 0;
 
   Piece<RT, WIDE> r[NCH];
   Piece<bf16, WIDE> y[NCH];
@@ -227,13 +222,20 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
   fetch(row0);
   for (int64_t row = row0; row < row1; ++row) {
     if (row >= sample_end) {
-      sample = row / p.tokens;
+      const int64_t sample = row / p.tokens;
       sample_end = (sample + 1) * p.tokens;
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
+        float w[8];
         load_vector<WIDE>(p.gate ? p.gate + sample * p.ldgate : nullptr, gate[j], 1.0f, j, n, lane, c);
         load_vector<WIDE>(p.scale ? p.scale + sample * p.ldscale : nullptr, scale[j], 0.0f, j, n, lane, c);
         load_vector<WIDE>(p.shift ? p.shift + sample * p.ldshift : nullptr, shift[j], 0.0f, j, n, lane, c);
+        load_vector<WIDE>(p.post_weight, w, 1.0f, j, n, lane, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gate[j][e] *= p.residual_scale * w[e];
+        load_vector<WIDE>(p.pre_weight, w, 1.0f, j, n, lane, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) scale[j][e] = (1.0f + scale[j][e]) * w[e];
       }
     }
     float x[NCH][8], z[NCH][8];
@@ -252,13 +254,13 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
 #pragma unroll
         for (int j = 0; j < NCH; ++j)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[j][e] = (z[j][e] - mean2) * rstd2 * wpost[j][e];
+          for (int e = 0; e < 8; ++e) z[j][e] = (z[j][e] - mean2) * rstd2;
       }
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[j][e] = __builtin_fmaf(p.residual_scale * gate[j][e], z[j][e], x[j][e]);
+          x[j][e] = __builtin_fmaf(gate[j][e], z[j][e], x[j][e]);
           // The norm is taken of the stream as it is stored.
           x[j][e] = static_cast<float>(static_cast<RT>(x[j][e]));
           if (!inside<WIDE>(j, e, n, lane, c)) x[j][e] = 0.0f;
@@ -272,8 +274,7 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
       for (int j = 0; j < NCH; ++j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          x[j][e] = __builtin_fmaf((x[j][e] - mean) * rstd * wpre[j][e], 1.0f + scale[j][e],
-                                   shift[j][e]);
+          x[j][e] = __builtin_fmaf((x[j][e] - mean) * rstd, scale[j][e], shift[j][e]);
         store_piece<WIDE>(static_cast<bf16*>(p.h) + row * p.ldh, x[j], j, n, lane, c);
       }
     }
@@ -468,73 +469,127 @@ __global__ __launch_bounds__(NCH == 1 ? 768 : 512) void residual_norm_bwd_kernel
   }
 }
 
-constexpr int kSumLanes = 8;  // partials read side by side for one channel
+// The sums of the partials: 16 VEC channels a workgroup, 64 partials side by side
+// (four in a wave, added by cross-lane moves; 16 waves, added in order).
+// blockIdx.y below p.sample_rows: a sample's three sums (samples y, y + sample_rows,
+// ...).  blockIdx.y == p.sample_rows: the weights' gradients, over the partials of
+// all samples.
+constexpr int kSumWaves = 16;
+constexpr int kSumLanes = 4 * kSumWaves;
 
-// A sample's partials, added: 64 channels a workgroup, kSumLanes partials at a
-// time, then the lanes in order.
-__global__ __launch_bounds__(64 * kSumLanes) void residual_norm_sums_kernel(
-    ResidualNormBwdParams p) {
-  __shared__ float part[3][kSumLanes][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
-  for (int64_t sample = blockIdx.y; sample < p.samples; sample += gridDim.y) {
-    const int64_t begin = sample * p.tokens;
-    const int64_t end = begin + p.tokens < p.m ? begin + p.tokens : p.m;
-    const int64_t w1 = (end - 1) / p.rows;
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    if (col < p.c) {
-      for (int64_t w = begin / p.rows + k; w <= w1; w += kSumLanes) {
-        const float* in = p.part + (w + sample) * 3 * p.c + col;
+template <int VEC>
+__device__ inline void load_cols(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const vec_t<float, 4> x = *reinterpret_cast<const vec_t<float, 4>*>(p);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) s[i] += in[static_cast<int64_t>(i) * p.c];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) part[i][k][threadIdx.x & 63] = s[i];
-    __syncthreads();
-    if (k < 3) {  // wave i adds up and writes sum i
-      float t = 0.0f;
-#pragma unroll
-      for (int l = 0; l < kSumLanes; ++l) t += part[k][l][threadIdx.x & 63];
-      if (col < p.c) {
-        const int64_t at = sample * p.c + col;
-        if (k == 0) {
-          if (p.dscale) p.dscale[at] = t * (p.pre_weight ? p.pre_weight[col] : 1.0f);
-          if (p.dpre_weight)
-            p.totals[at] = t * (1.0f + (p.scale ? p.scale[sample * p.ldscale + col] : 0.0f));
-        } else if (k == 1) {
-          const float a = p.residual_scale * t;
-          if (p.dgate) p.dgate[at] = a * (p.post_weight ? p.post_weight[col] : 1.0f);
-          if (p.dpost_weight)
-            p.totals[(p.samples + sample) * p.c + col] =
-                a * (p.gate ? p.gate[sample * p.ldgate + col] : 1.0f);
-        } else if (p.dshift) {
-          p.dshift[at] = t;
-        }
-      }
-    }
-    __syncthreads();
+    for (int e = 0; e < 4; ++e) v[e] = x[e];
+  } else {
+    v[0] = p[0];
   }
 }
+template <int VEC>
+__device__ inline void store_cols(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<vec_t<float, 4>*>(p) = vec_t<float, 4>{v[0], v[1], v[2], v[3]};
+  else
+    p[0] = v[0];
+}
 
-// The weights' gradients: the samples' shares, added; blockIdx.y picks the weight.
-__global__ __launch_bounds__(64 * kSumLanes) void residual_norm_weights_kernel(
+template <int VEC>
+__global__ __launch_bounds__(64 * kSumWaves) void residual_norm_sums_kernel(
     ResidualNormBwdParams p) {
-  float* out = blockIdx.y ? p.dpost_weight : p.dpre_weight;
-  if (out == nullptr) return;
-  __shared__ float part[kSumLanes][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
-  const float* in = p.totals + static_cast<int64_t>(blockIdx.y) * p.samples * p.c;
-  float s = 0.0f;
-  if (col < p.c)
-    for (int64_t i = k; i < p.samples; i += kSumLanes) s += in[i * p.c + col];
-  part[k][threadIdx.x & 63] = s;
-  __syncthreads();
-  if (k == 0 && col < p.c) {
-    s = 0.0f;
+  __shared__ float part[3][kSumWaves][16 * VEC];
+  const int lane = threadIdx.x & 15, wave = threadIdx.x >> 6;
+  const int k = threadIdx.x >> 4;  // of 64 partials side by side
+  const int64_t c = p.c;
+  const int col = (blockIdx.x * 16 + lane) * VEC;
+  const bool in = col < c;
+  // All partials' sums; those of sum i arrive in the first 16 lanes of wave i < 3.
+  auto join = [&](float (&s)[3][VEC], float (&t)[VEC]) {
+    __syncthreads();
 #pragma unroll
-    for (int l = 0; l < kSumLanes; ++l) s += part[l][threadIdx.x & 63];
-    out[col] = s;
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        s[i][e] += __shfl_xor(s[i][e], 16);
+        s[i][e] += __shfl_xor(s[i][e], 32);
+        part[i][wave][lane * VEC + e] = s[i][e];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      t[e] = 0.0f;
+      if (wave < 3) {
+#pragma unroll
+        for (int l = 0; l < kSumWaves; ++l) t[e] += part[wave][l][lane * VEC + e];
+      }
+    }
+  };
+  const bool writes = in && (threadIdx.x & 48) == 0;
+  auto vector_at = [&](const float* v, float none, float (&x)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = v ? v[col + e] : none;
+  };
+  if (blockIdx.y < p.sample_rows) {
+    for (int64_t sample = blockIdx.y; sample < p.samples; sample += p.sample_rows) {
+      const int64_t begin = sample * p.tokens;
+      const int64_t end = begin + p.tokens < p.m ? begin + p.tokens : p.m;
+      const int64_t w1 = (end - 1) / p.rows;
+      float s[3][VEC] = {}, t[VEC], f[VEC];
+      if (in)
+        for (int64_t w = begin / p.rows + k; w <= w1; w += kSumLanes)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            load_cols<VEC>(p.part + ((w + sample) * 3 + i) * c + col, f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[i][e] += f[e];
+          }
+      join(s, t);
+      if (!writes) continue;
+      const int64_t at = sample * c + col;
+      if (wave == 0 && p.dscale) {
+        vector_at(p.pre_weight, 1.0f, f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) t[e] *= f[e];
+        store_cols<VEC>(p.dscale + at, t);
+      } else if (wave == 1 && p.dgate) {
+        vector_at(p.post_weight, 1.0f, f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) t[e] *= p.residual_scale * f[e];
+        store_cols<VEC>(p.dgate + at, t);
+      } else if (wave == 2 && p.dshift) {
+        store_cols<VEC>(p.dshift + at, t);
+      }
+    }
+    return;
   }
+  const int64_t groups = p.m > 0 ? (p.m + p.rows - 1) / p.rows : 0;
+  float s[3][VEC] = {}, t[VEC];
+  if (in)
+    for (int64_t w = k; w < groups; w += kSumLanes) {
+      // (Rows fit 32 bits; so does a sample's length, cut to them.)
+      const uint32_t first = static_cast<uint32_t>(w * p.rows);
+      const int64_t last = (w + 1) * p.rows < p.m ? (w + 1) * p.rows : p.m;
+      const uint32_t tokens = static_cast<uint32_t>(p.tokens < p.m ? p.tokens : p.m);
+      for (int64_t sample = first / tokens; sample * p.tokens < last; ++sample) {
+        float f[VEC], g[VEC];
+        load_cols<VEC>(p.part + (w + sample) * 3 * c + col, f);
+        vector_at(p.scale ? p.scale + sample * p.ldscale : nullptr, 0.0f, g);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s[0][e] = __builtin_fmaf(1.0f + g[e], f[e], s[0][e]);
+        load_cols<VEC>(p.part + ((w + sample) * 3 + 1) * c + col, f);
+        vector_at(p.gate ? p.gate + sample * p.ldgate : nullptr, 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          s[1][e] = __builtin_fmaf(p.residual_scale * g[e], f[e], s[1][e]);
+      }
+    }
+  join(s, t);
+  if (!writes) return;
+  if (wave == 0 && p.dpre_weight)
+    store_cols<VEC>(p.dpre_weight + col, t);
+  else if (wave == 1 && p.dpost_weight)
+    store_cols<VEC>(p.dpost_weight + col, t);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -611,20 +666,31 @@ hipError_t launch_residual_norm(ResidualNormParams& p, bool r_is_bf16, hipStream
 
 int64_t residual_norm_bwd_workspace(int64_t m, int64_t c, int64_t tokens) {
   if (m == 0) return 0;
+  // Partials of every (workgroup, sample).
   const BwdPlan b = plan_bwd(m, c, tokens);
-  // Partials of every (workgroup, sample) and the samples' shares of the two weights,
-  // the second part from a 16-byte boundary.
-  return ((b.groups + b.samples) * 3 * c + 3 + 2 * b.samples * c) * 4;
+  return (b.groups + b.samples) * 3 * c * 4;
+}
+
+hipError_t launch_sums(const ResidualNormBwdParams& p, hipStream_t stream) {
+  const bool wide = p.c % 4 == 0 && aligned16(p.dgate) && aligned16(p.dscale) &&
+                    aligned16(p.dshift) && aligned16(p.dpre_weight) && aligned16(p.dpost_weight);
+  const int cols = wide ? 64 : 16;
+  const dim3 grid(static_cast<unsigned>((p.c + cols - 1) / cols),
+                  p.sample_rows + (p.dpre_weight || p.dpost_weight ? 1u : 0u));
+  if (grid.y == 0) return hipSuccess;
+  if (wide)
+    hipLaunchKernelGGL((residual_norm_sums_kernel<4>), grid, dim3(64 * kSumWaves), 0, stream, p);
+  else
+    hipLaunchKernelGGL((residual_norm_sums_kernel<1>), grid, dim3(64 * kSumWaves), 0, stream, p);
+  return hipGetLastError();
 }
 
 hipError_t launch_residual_norm_bwd(ResidualNormBwdParams& p, bool r_is_bf16, void* workspace,
                                     hipStream_t stream) {
-  if (p.m == 0) {
+  if (p.m == 0) {  // empty sums
     p.samples = 0;
-    if (p.dpre_weight || p.dpost_weight)
-      hipLaunchKernelGGL(residual_norm_weights_kernel, dim3((p.c + 63) / 64, 2),
-                         dim3(64 * kSumLanes), 0, stream, p);
-    return hipGetLastError();
+    p.sample_rows = 0;
+    return launch_sums(p, stream);
   }
   const BwdPlan b = plan_bwd(p.m, p.c, p.tokens);
   p.threads = 64 * b.waves;
@@ -633,7 +699,9 @@ hipError_t launch_residual_norm_bwd(ResidualNormBwdParams& p, bool r_is_bf16, vo
   p.samples = b.samples;
   const bool sums = p.dgate || p.dscale || p.dshift || p.dpre_weight || p.dpost_weight;
   p.part = sums ? static_cast<float*>(workspace) : nullptr;
-  p.totals = static_cast<float*>(workspace) + ((b.groups + b.samples) * 3 * p.c + 3) / 4 * 4;
+  p.sample_rows = !(p.dgate || p.dscale || p.dshift) ? 0u
+                  : p.samples < 32768                ? static_cast<uint32_t>(p.samples)
+                                                     : 32768u;
   const bool wide = p.c % 8 == 0 && p.lddro % 8 == 0 && aligned16(p.dr_out) && p.lddh % 8 == 0 &&
                     aligned16(p.dh) && p.ldro % 8 == 0 && aligned16(p.r_out) && p.ldy % 8 == 0 &&
                     aligned16(p.y) && p.lddr % 8 == 0 && aligned16(p.dr) && p.lddy % 8 == 0 &&
@@ -646,15 +714,7 @@ hipError_t launch_residual_norm_bwd(ResidualNormBwdParams& p, bool r_is_bf16, vo
   else
     e = wide ? launch_bwd<float, true>(p, b, stream) : launch_bwd<float, false>(p, b, stream);
   if (e != hipSuccess || !sums) return e;
-  const unsigned cols = static_cast<unsigned>((p.c + 63) / 64);
-  const unsigned samples = static_cast<unsigned>(p.samples < 65535 ? p.samples : 65535);
-  hipLaunchKernelGGL(residual_norm_sums_kernel, dim3(cols, samples), dim3(64 * kSumLanes), 0,
-                     stream, p);
-  e = hipGetLastError();
-  if (e != hipSuccess || !(p.dpre_weight || p.dpost_weight)) return e;
-  hipLaunchKernelGGL(residual_norm_weights_kernel, dim3(cols, 2), dim3(64 * kSumLanes), 0, stream,
-                     p);
-  return hipGetLastError();
+  return launch_sums(p, stream);
 }
 
 }  // namespace tern
