@@ -18,7 +18,8 @@
 // Statistics are in fp32 and centred: a wave takes its own mean and the
 // squares about it, and the waves' are joined by the shift formula
 // sum (x - m)^2 = sum_w (Q_w + n_w (m_w - m)^2), so that a stream with a large
-// mean loses nothing.
+// mean loses nothing (m_w need only be near the wave's mean: the difference's own
+// term is kept).
 //
 // Backward, the sums over rows are S = sum dh n, Z = sum dr zn and H = sum dh:
 // dscale = w_pre S, dgate = alpha w_post Z, dshift = H, and the weights'
@@ -134,61 +135,73 @@ __device__ inline bool inside(int j, int e, int n, int lane, int c) {
   return (WIDE ? 8 * (j * n + lane) : (8 * j + e) * n + lane) < c;
 }
 
-// Sums over a row's waves: each wave leaves its own in LDS, two buffers in turn
-// so that one barrier a sum is enough (a wave can be at most one sum ahead of
-// the slowest reader).  `waves` waves from `first` on share a row.
+// Sums over a row's waves (at most eight): each wave leaves its own in LDS and lane w
+// of every eight takes wave w's, for eight_sum.  Two buffers in turn, so that one
+// barrier a sum is enough (a wave can be at most one sum ahead of the slowest
+// reader).  `waves` waves from `first` on share a row.
 struct RowSums {
   float4 (*buf)[kMaxWaves];
   int first, waves, wave, turn;
-  __device__ const float4* meet(float4 mine) {
+  __device__ float4 meet(float4 mine) {
     float4* b = buf[turn & 1];
     ++turn;
     if ((threadIdx.x & 63) == 0) b[wave] = mine;
     __syncthreads();
-    return b + first;
+    const int w = threadIdx.x & 7;
+    return w < waves ? b[first + w] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
 };
 
+// How many of a row's channels the lane's wave holds.
+template <int NCH, bool WIDE>
+__device__ inline float channels_of_wave(int n, int lane, int c) {
+  float own = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) own += inside<WIDE>(j, e, n, lane, c) ? 1.0f : 0.0f;
+  return wave_sum(own);
+}
+
 // mean and 1 / sqrt(variance or mean square + eps) of a row of c values, held
-// eight by eight; values past the end are 0.
+// eight by eight; values past the end are 0.  own: channels_of_wave.
 template <int NCH, bool WIDE>
 __device__ inline void statistics(const float (&x)[NCH][8], bool layer, float eps, int n, int lane,
-                                  int c, RowSums& sums, float& mean, float& rstd) {
-  float s = 0.0f, own = 0.0f;
+                                  int c, float own, RowSums& sums, float& mean, float& rstd) {
+  float s = 0.0f, centre = 0.0f;
   if (layer) {
 #pragma unroll
     for (int j = 0; j < NCH; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s += x[j][e];
-        own += inside<WIDE>(j, e, n, lane, c) ? 1.0f : 0.0f;
-      }
+      for (int e = 0; e < 8; ++e) s += x[j][e];
     s = wave_sum(s);
-    own = wave_sum(own);
+    centre = own > 0.0f ? s * __builtin_amdgcn_rcpf(own) : 0.0f;  // any value near the mean does
   }
-  const float centre = layer && own > 0.0f ? s / own : 0.0f;
   float q = 0.0f;
 #pragma unroll
-  for (int j = 0; j < NCH; ++j)
+  for (int j = 0; j < NCH; ++j) {
+    float piece = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float d = inside<WIDE>(j, e, n, lane, c) ? x[j][e] - centre : 0.0f;
-      q = __builtin_fmaf(d, d, q);
+      const float d = WIDE || inside<WIDE>(j, e, n, lane, c) ? x[j][e] - centre : 0.0f;
+      piece = __builtin_fmaf(d, d, piece);
     }
+    // (A wide piece is all inside or all past the end.)
+    q += !WIDE || inside<WIDE>(j, 0, n, lane, c) ? piece : 0.0f;
+  }
   q = wave_sum(q);
   const float inv = 1.0f / static_cast<float>(c);
   if (sums.waves > 1) {
-    const float4* b = sums.meet(make_float4(s, own, centre, q));
-    float total = 0.0f;
-    for (int w = 0; w < sums.waves; ++w) total += b[w].x;
-    mean = total * inv;
-    q = 0.0f;
-    for (int w = 0; w < sums.waves; ++w) {
-      const float d = b[w].z - mean;
-      q += b[w].w + b[w].y * d * d;  // y is 0 without a mean
-    }
+    // sum (x - mean)^2 = sum (x - centre)^2 - 2 (mean - centre) sum (x - centre) + n (mean - centre)^2,
+    // the middle sum being s - n centre.
+    const float4 w = sums.meet(make_float4(s, own, centre, q));
+    mean = eight_sum(w.x) * inv;
+    const float d = mean - w.z;
+    q = eight_sum(w.w + d * (w.y * d - 2.0f * (w.x - w.y * w.z)));
   } else {
     mean = s * inv;
+    const float d = mean - centre;
+    q += d * (own * d - 2.0f * (s - own * centre));
   }
   const float v = __builtin_fmaf(q, inv, eps);
   // One Newton step after the hardware's reciprocal square root.
@@ -209,6 +222,7 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
   // Of the row's sample: alpha gate w_post, w_pre (1 + scale), shift.
   float gate[NCH][8], scale[NCH][8], shift[NCH][8];
   int64_t sample_end = 0;
+  const float own = channels_of_wave<NCH, WIDE>(n, lane, c);
 
   Piece<RT, WIDE> r[NCH];
   Piece<bf16, WIDE> y[NCH];
@@ -232,7 +246,8 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
         load_vector<WIDE>(p.shift ? p.shift + sample * p.ldshift : nullptr, shift[j], 0.0f, j, n, lane, c);
         load_vector<WIDE>(p.post_weight, w, 1.0f, j, n, lane, c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gate[j][e] *= p.residual_scale * w[e];
+        for (int e = 0; e < 8; ++e)  // (0 past the end keeps the stream's lanes there 0)
+          gate[j][e] = inside<WIDE>(j, e, n, lane, c) ? gate[j][e] * p.residual_scale * w[e] : 0.0f;
         load_vector<WIDE>(p.pre_weight, w, 1.0f, j, n, lane, c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) scale[j][e] = (1.0f + scale[j][e]) * w[e];
@@ -250,7 +265,8 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
     float mean = 0.0f, rstd = 0.0f, mean2 = 0.0f, rstd2 = 0.0f;
     if (has_y) {
       if (p.post != TERN_NORM_NONE) {
-        statistics<NCH, WIDE>(z, p.post == TERN_NORM_LAYER, p.eps, n, lane, c, sums, mean2, rstd2);
+        statistics<NCH, WIDE>(z, p.post == TERN_NORM_LAYER, p.eps, n, lane, c, own, sums, mean2,
+                              rstd2);
 #pragma unroll
         for (int j = 0; j < NCH; ++j)
 #pragma unroll
@@ -263,13 +279,12 @@ __global__ __launch_bounds__(512) void residual_norm_kernel(ResidualNormParams p
           x[j][e] = __builtin_fmaf(gate[j][e], z[j][e], x[j][e]);
           // The norm is taken of the stream as it is stored.
           x[j][e] = static_cast<float>(static_cast<RT>(x[j][e]));
-          if (!inside<WIDE>(j, e, n, lane, c)) x[j][e] = 0.0f;
         }
         store_piece<WIDE>(static_cast<RT*>(p.r_out) + row * p.ldro, x[j], j, n, lane, c);
       }
     }
     if (has_h) {
-      statistics<NCH, WIDE>(x, p.pre == TERN_NORM_LAYER, p.eps, n, lane, c, sums, mean, rstd);
+      statistics<NCH, WIDE>(x, p.pre == TERN_NORM_LAYER, p.eps, n, lane, c, own, sums, mean, rstd);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
 #pragma unroll
@@ -299,12 +314,9 @@ __device__ inline void through_norm(float (&g)[NCH][8], const float (&x)[NCH][8]
   a = wave_sum(a);
   b = wave_sum(b);
   if (sums.waves > 1) {
-    const float4* w = sums.meet(make_float4(a, b, 0.0f, 0.0f));
-    a = b = 0.0f;
-    for (int i = 0; i < sums.waves; ++i) {
-      a += w[i].x;
-      b += w[i].y;
-    }
+    const float4 w = sums.meet(make_float4(a, b, 0.0f, 0.0f));
+    a = eight_sum(w.x);
+    b = eight_sum(w.y);
   }
   const float inv = 1.0f / static_cast<float>(c);
   a *= inv;

@@ -37,4 +37,11 @@ __device__ inline float wave_sum(float x) {
   return lo + hi;
 }
 
+// The sum over each aligned group of eight lanes, in every lane.
+__device__ inline float eight_sum(float x) {
+  x += dpp_move<0xB1>(x);
+  x += dpp_move<0x4E>(x);
+  return x + dpp_move<0x141>(x);
+}
+
 }  // namespace tern
