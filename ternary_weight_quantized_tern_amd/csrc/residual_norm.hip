@@ -116,6 +116,24 @@ __device__ inline void store_piece(T* row, const float (&v)[8], int j, int n, in
   }
 }
 
+template <int VEC>
+__device__ inline void load_cols(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const vec_t<float, 4> x = *reinterpret_cast<const vec_t<float, 4>*>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = x[e];
+  } else {
+    v[0] = p[0];
+  }
+}
+template <int VEC>
+__device__ inline void store_cols(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<vec_t<float, 4>*>(p) = vec_t<float, 4>{v[0], v[1], v[2], v[3]};
+  else
+    p[0] = v[0];
+}
+
 // Eight channels of a per-channel vector, `none` where there is no vector and
 // past its end.
 template <bool WIDE>
@@ -335,7 +353,7 @@ template <typename RT, int NCH, bool WIDE>
 __global__ __launch_bounds__(NCH == 1 ? 768 : 512) void residual_norm_bwd_kernel(
     ResidualNormBwdParams p) {
   __shared__ float4 meet[2][kMaxWaves];
-  extern __shared__ float joined[];  // [3][8 NCH threads] with more than one slot
+  extern __shared__ __attribute__((aligned(16))) float joined[];  // [slots][3][c] with more than one
   const int n = p.threads, c = p.c;
   const int slot = threadIdx.x / n, lane = threadIdx.x - slot * n;
   RowSums sums{meet, slot * (n >> 6), n >> 6, static_cast<int>(threadIdx.x >> 6), 0};
@@ -442,38 +460,35 @@ __global__ __launch_bounds__(NCH == 1 ? 768 : 512) void residual_norm_bwd_kernel
       }
     }
     if (p.part != nullptr) {
-      // The slots' sums, added in the slots' order.
-      for (int k = 1; k < p.slots; ++k) {
-        __syncthreads();
-        if (slot == k) {
-#pragma unroll
-          for (int j = 0; j < NCH; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              joined[(8 * j + e) * n + lane] = sum_n[j][e];
-              joined[(8 * (NCH + j) + e) * n + lane] = sum_z[j][e];
-              joined[(8 * (2 * NCH + j) + e) * n + lane] = sum_h[j][e];
-            }
-        }
-        __syncthreads();
-        if (slot == 0) {
-#pragma unroll
-          for (int j = 0; j < NCH; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              sum_n[j][e] += joined[(8 * j + e) * n + lane];
-              sum_z[j][e] += joined[(8 * (NCH + j) + e) * n + lane];
-              sum_h[j][e] += joined[(8 * (2 * NCH + j) + e) * n + lane];
-            }
-        }
-      }
-      if (slot == 0) {
-        float* out = p.part + (static_cast<int64_t>(blockIdx.x) + sample) * 3 * c;
+      float* out = p.part + (static_cast<int64_t>(blockIdx.x) + sample) * 3 * c;
+      if (p.slots == 1) {
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
           store_piece<WIDE>(out, sum_n[j], j, n, lane, c);
           store_piece<WIDE>(out + c, sum_z[j], j, n, lane, c);
           store_piece<WIDE>(out + 2 * c, sum_h[j], j, n, lane, c);
+        }
+      } else {
+        // All slots' sums side by side in LDS, then added in the slots' order.
+        const int pitch = (c + 3) & ~3;
+        float* mine = joined + slot * 3 * pitch;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+          store_piece<WIDE>(mine, sum_n[j], j, n, lane, c);
+          store_piece<WIDE>(mine + pitch, sum_z[j], j, n, lane, c);
+          store_piece<WIDE>(mine + 2 * pitch, sum_h[j], j, n, lane, c);
+        }
+        __syncthreads();
+        constexpr int kVec = WIDE ? 4 : 1;
+        for (int x = threadIdx.x * kVec; x < 3 * pitch; x += blockDim.x * kVec) {
+          const int i = x / pitch, col = x - i * pitch;
+          if (col >= c) continue;
+          float t[kVec] = {};
+          for (int k = 0; k < p.slots; ++k)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) t[e] += joined[k * 3 * pitch + x + e];
+          store_cols<kVec>(out + i * static_cast<int64_t>(c) + col, t);
         }
       }
     }
@@ -488,24 +503,6 @@ __global__ __launch_bounds__(NCH == 1 ? 768 : 512) void residual_norm_bwd_kernel
 // all samples.
 constexpr int kSumWaves = 16;
 constexpr int kSumLanes = 4 * kSumWaves;
-
-template <int VEC>
-__device__ inline void load_cols(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 4) {
-    const vec_t<float, 4> x = *reinterpret_cast<const vec_t<float, 4>*>(p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = x[e];
-  } else {
-    v[0] = p[0];
-  }
-}
-template <int VEC>
-__device__ inline void store_cols(float* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 4)
-    *reinterpret_cast<vec_t<float, 4>*>(p) = vec_t<float, 4>{v[0], v[1], v[2], v[3]};
-  else
-    p[0] = v[0];
-}
 
 template <int VEC>
 __global__ __launch_bounds__(64 * kSumWaves) void residual_norm_sums_kernel(
@@ -576,26 +573,34 @@ __global__ __launch_bounds__(64 * kSumWaves) void residual_norm_sums_kernel(
     return;
   }
   const int64_t groups = p.m > 0 ? (p.m + p.rows - 1) / p.rows : 0;
+  // (Rows fit 32 bits; so does a sample's length, cut to them.)
+  const uint32_t tokens = static_cast<uint32_t>(p.tokens < p.m ? p.tokens : p.m);
   float s[3][VEC] = {}, t[VEC];
-  if (in)
-    for (int64_t w = k; w < groups; w += kSumLanes) {
-      // (Rows fit 32 bits; so does a sample's length, cut to them.)
-      const uint32_t first = static_cast<uint32_t>(w * p.rows);
-      const int64_t last = (w + 1) * p.rows < p.m ? (w + 1) * p.rows : p.m;
-      const uint32_t tokens = static_cast<uint32_t>(p.tokens < p.m ? p.tokens : p.m);
-      for (int64_t sample = first / tokens; sample * p.tokens < last; ++sample) {
-        float f[VEC], g[VEC];
-        load_cols<VEC>(p.part + (w + sample) * 3 * c + col, f);
-        vector_at(p.scale ? p.scale + sample * p.ldscale : nullptr, 0.0f, g);
+  auto add = [&](int64_t w, int64_t sample) {
+    float f[2][VEC], g[2][VEC];
+    load_cols<VEC>(p.part + (w + sample) * 3 * c + col, f[0]);
+    load_cols<VEC>(p.part + ((w + sample) * 3 + 1) * c + col, f[1]);
+    vector_at(p.scale ? p.scale + sample * p.ldscale : nullptr, 0.0f, g[0]);
+    vector_at(p.gate ? p.gate + sample * p.ldgate : nullptr, 1.0f, g[1]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s[0][e] = __builtin_fmaf(1.0f + g[e], f[e], s[0][e]);
-        load_cols<VEC>(p.part + ((w + sample) * 3 + 1) * c + col, f);
-        vector_at(p.gate ? p.gate + sample * p.ldgate : nullptr, 1.0f, g);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          s[1][e] = __builtin_fmaf(p.residual_scale * g[e], f[e], s[1][e]);
-      }
+    for (int e = 0; e < VEC; ++e) {
+      s[0][e] = __builtin_fmaf(1.0f + g[0][e], f[0][e], s[0][e]);
+      s[1][e] = __builtin_fmaf(p.residual_scale * g[1][e], f[1][e], s[1][e]);
     }
+  };
+  if (in) {
+    // The workgroup's first sample for four workgroups at a time (their loads go out
+    // together), then the others that begin in it.
+#pragma unroll 4
+    for (int64_t w = k; w < groups; w += kSumLanes)
+      add(w, static_cast<uint32_t>(w * p.rows) / tokens);
+    for (int64_t w = k; w < groups; w += kSumLanes) {
+      const int64_t last = (w + 1) * p.rows < p.m ? (w + 1) * p.rows : p.m;
+      for (int64_t sample = static_cast<uint32_t>(w * p.rows) / tokens + 1; sample * tokens < last;
+           ++sample)
+        add(w, sample);
+    }
+  }
   join(s, t);
   if (!writes) return;
   if (wave == 0 && p.dpre_weight)
@@ -648,7 +653,7 @@ hipError_t launch_fwd(ResidualNormParams& p, int pieces, hipStream_t stream) {
 template <typename RT, bool WIDE>
 hipError_t launch_bwd(ResidualNormBwdParams& p, const BwdPlan& b, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(b.groups)), block(p.threads * b.slots);
-  const unsigned lds = b.slots > 1 ? 3u * 8u * b.pieces * p.threads * 4u : 0u;
+  const unsigned lds = b.slots > 1 ? b.slots * 3u * ((p.c + 3) & ~3) * 4u : 0u;
   if (b.pieces == 1)
     hipLaunchKernelGGL((residual_norm_bwd_kernel<RT, 1, WIDE>), grid, block, lds, stream, p);
   else
