@@ -1,0 +1,200 @@
+"""The transformer-block operators together: the example block against the same
+block in plain fp32 torch, forward and backward; replays of captured graphs
+and calls on other streams against eager results.
+"""
+from __future__ import annotations
+
+import importlib.util
+import math
+import os
+
+import pytest
+import torch
+
+from parity import DEV, log
+
+pytestmark = pytest.mark.gpu
+tern = pytest.importorskip("ternary_weight_quantized_tern_amd")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def example():
+    path = os.path.join(ROOT, "examples", "text_conditioned_block.py")
+    spec = importlib.util.spec_from_file_location("text_conditioned_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+class _Ternary(torch.autograd.Function):
+    """The ternary layer in fp32 with the straight-through gradient."""
+
+    @staticmethod
+    def forward(ctx, x, w):
+        s = w.abs().mean(1, keepdim=True)
+        wq = torch.where(2 * w.abs() > s, w.sign(), torch.zeros_like(w)) * s
+        ctx.save_for_backward(x, wq)
+        return x @ wq.T
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, wq = ctx.saved_tensors
+        return dy @ wq, dy.T @ x
+
+
+def plain_block(block, ex, x, caption, mask, positions, conditioning):
+    b, t, c = x.shape
+    heads, width = block.heads, block.width
+    mod = block.modulation(conditioning).split(c, dim=1)
+    lin = lambda v, w: _Ternary.apply(v.reshape(-1, c if v.shape[-1] == c else v.shape[-1]), w)  # noqa: E731
+
+    def norm(r, scale, shift):
+        n = (r - r.mean(-1, keepdim=True)) / torch.sqrt(r.var(-1, unbiased=False, keepdim=True) + 1e-6)
+        return n * (1 + scale[:, None]) + shift[:, None]
+
+    def attend(q, k, v, keep):
+        s = torch.einsum("bqhd,bkhd->bhqk", q, k) / math.sqrt(width)
+        if keep is not None:
+            s = s.masked_fill(~keep[:, None, None], -math.inf)
+            p = torch.softmax(s, -1).nan_to_num()
+        else:
+            p = torch.softmax(s, -1)
+        return torch.einsum("bhqk,bkhd->bqhd", p, v).reshape(-1, c)
+
+    h = norm(x, mod[0], mod[1])
+    qkv = lin(h, block.qkv).view(b, t, 3 * heads, width)
+    turn = torch.cat([10000.0 ** (-torch.arange(0, n, 2, device=DEV, dtype=torch.float64) / n)
+                      for n in block.axes])
+    axis = torch.repeat_interleave(torch.arange(3, device=DEV),
+                                   torch.tensor(block.axes, device=DEV) // 2)
+    angle = (positions.double()[:, axis] * turn)[None, :, None]
+    cos, sin = angle.cos().float(), angle.sin().float()
+    qk = qkv[:, :, :2 * heads]
+    u, v_ = qk[..., 0::2], qk[..., 1::2]
+    qk = torch.stack([u * cos - v_ * sin, u * sin + v_ * cos], -1).flatten(-2)
+    y = lin(attend(qk[:, :, :heads], qk[:, :, heads:], qkv[:, :, 2 * heads:], None), block.out)
+    r = x + mod[2][:, None] * y.view(b, t, c)
+    q = lin(norm(r, mod[3], mod[4]), block.cross_q).view(b, t, heads, width)
+    kv = lin(caption, block.cross_kv).view(b, -1, 2 * heads, width)
+    y = lin(attend(q, kv[:, :, :heads], kv[:, :, heads:], mask), block.cross_out)
+    r = r + mod[5][:, None] * y.view(b, t, c)
+    y = torch.nn.functional.gelu(lin(norm(r, mod[6], mod[7]), block.up), approximate="tanh")
+    y = _Ternary.apply(y, block.down)
+    return r + mod[8][:, None] * y.view(b, t, c)
+
+
+def test_example_block_matches_plain_torch():
+    log("block example against plain torch")
+    ex = example()
+    torch.manual_seed(1)
+    hidden, heads, b, grid, s = 192, 2, 3, (2, 5, 7), 21
+    block = ex.Block(hidden, heads, 64).to(DEV)
+    t = grid[0] * grid[1] * grid[2]
+    x = torch.randn(b, t, hidden, device=DEV)
+    caption = torch.randn(b, s, hidden, device=DEV).to(torch.bfloat16)
+    mask = torch.arange(s, device=DEV)[None] < torch.tensor([[s], [4], [0]], device=DEV)
+    cond = torch.randn(b, 64, device=DEV)
+    pos = ex.grid_positions(*grid, DEV)
+    out = block(x, caption, mask, pos, cond)
+    dout = torch.randn(b, t, hidden, device=DEV)
+    out.backward(dout)
+    got = {n: p.grad.clone() for n, p in block.named_parameters()}
+    block.zero_grad()
+    ref = plain_block(block, ex, x, caption.float(), mask, pos, cond)
+    ref.backward(dout)
+    # Some ten bf16 roundings of 2^-9 (rms) lie on the way out and twenty on the way
+    # of a gradient, through layers that keep sizes within a factor of two: 2^-5 and
+    # 2^-4 of the whole.
+    off = float((out - ref).norm() / (ref - x).norm())
+    assert off < 2.0 ** -5, off
+    for n, p in block.named_parameters():
+        off = float((got[n] - p.grad).norm() / p.grad.norm())
+        assert off < 2.0 ** -4, (n, off)
+
+
+def test_example_trains():
+    log("block example trains")
+    losses = example().train(steps=8, hidden=192, heads=2, batch=2, grid=(1, 6, 6), states=17)
+    assert all(math.isfinite(v) for v in losses) and losses[-1] < 0.95 * losses[0]
+
+
+def calls(seed):
+    """Each operator once, forward and backward, on inputs of this seed: a list of
+    argument tensors and a function of them."""
+    g = torch.Generator().manual_seed(seed)
+
+    def n(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=g).to(dtype).to(DEV)
+
+    q, k, v, do = n(2, 70, 6, 64), n(2, 300, 2, 64), n(2, 300, 2, 64), n(2, 70, 6, 64)
+    q1, mask = n(2, 1, 6, 64), (torch.rand(2, 300, generator=g) < 0.7).to(DEV)
+    r, y, dr, dh = n(60, 328, dtype=torch.float32), n(60, 328), n(60, 328, dtype=torch.float32), n(60, 328)
+    vec, w = n(4, 3 * 328, dtype=torch.float32), n(328, dtype=torch.float32)
+    pos = torch.randint(0, 40, (2, 70, 3), generator=g).float().to(DEV)
+    args = [q, k, v, do, q1, mask, r, y, dr, dh, vec, w, pos]
+
+    def run(q, k, v, do, q1, mask, r, y, dr, dh, vec, w, pos):
+        gate, scale, shift = vec.split(328, 1)
+        x = tern.rope(q, pos, (16, 24, 24))
+        o, lse = tern.attention(x, k, v, mask=mask)
+        grads = tern.attention_backward(do, x, k, v, o, lse, mask=mask)
+        o1, lse1 = tern.attention(q1, k, v, mask=mask)
+        opt = dict(tokens=15, pre="layer", post="rms", pre_weight=w, post_weight=w)
+        r_out, h, st = tern.residual_norm(r, y, gate=gate, scale=scale, shift=shift,
+                                          with_stats=True, **opt)
+        back = tern.residual_norm_backward(dr, dh, r_out, y, st, gate=gate, scale=scale, **opt)
+        return [x, o, lse, *grads, o1, lse1, r_out, h, st, *back]
+
+    return args, run
+
+
+def test_graph_replays_match_eager_results():
+    log("block operators in a graph")
+    args, run = calls(1)
+    for _ in range(2):
+        run(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(*args)
+    for seed in (2, 3, 4):
+        fresh, _ = calls(seed)
+        for a, f in zip(args, fresh):
+            a.copy_(f)
+        eager = run(*fresh)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, eager):
+            assert torch.equal(a, b), seed
+        _ = eager[0].float().sum().item()
+
+
+def test_two_streams_give_the_serial_results():
+    log("block operators on two streams")
+    args, run = zip(*[calls(s) for s in (5, 6)])
+    serial = [run[i](*args[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                out[i] = run[i](*args[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b in zip(out[i], serial[i]):
+            assert torch.equal(a, b)
+
+
+def test_named_stream_argument_is_used():
+    log("block operators on a named stream")
+    q = torch.randn(1, 8, 2, 64, device=DEV).to(torch.bfloat16)
+    pos = torch.zeros(1, 8, 1, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = tern.rope(q, pos, (64,), stream=side)
+    o, _ = tern.attention(q, q, q, stream=side)
+    side.synchronize()
+    assert torch.equal(a, q) and torch.equal(o, tern.attention(q, q, q)[0])
