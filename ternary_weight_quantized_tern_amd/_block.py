@@ -241,19 +241,25 @@ def residual_norm_backward(dr_out, dh, r_out: torch.Tensor, y, stats: torch.Tens
         raise ValueError(f"stats must be a contiguous [{m}, 4] tensor")
     dr = r_out.new_empty((m, c))
     dy = None if y is None else r_out.new_empty((m, c), dtype=torch.bfloat16)
-
-    def sums(wanted, *size):
-        """One tensor for each of `wanted` (None for those that are not), and their addresses."""
-        n = sum(wanted)
-        made = iter(r_out.new_empty((n, *size), dtype=torch.float32).unbind(0) if n else ())
-        out = [next(made) if w else None for w in wanted]
-        return out + [None if a is None else a.data_ptr() for a in out]
-
     with_y, with_h = y is not None, dh is not None
-    dgate, dscale, dshift, gp, scp, shp = sums(
-        (gate is not None and with_y, scale is not None and with_h, with_shift and with_h), samples, c)
-    dpre, dpost, prp, pop = sums(
-        (pre_weight is not None and with_h, post_weight is not None and with_y), c)
+    # The sums' tensors are rows of one: an allocation costs more than a view.
+    each = (gate is not None and with_y, scale is not None and with_h, with_shift and with_h)
+    whole = (pre_weight is not None and with_h, post_weight is not None and with_y)
+    rows = sum(each) * samples + sum(whole)
+    dgate = dscale = dshift = dpre = dpost = gp = scp = shp = prp = pop = None
+    if rows:
+        out = r_out.new_empty((rows, c), dtype=torch.float32)
+        at, step, row = out.data_ptr(), 4 * c * samples, 0
+        if each[0]:
+            dgate, gp, at, row = out[row:row + samples], at, at + step, row + samples
+        if each[1]:
+            dscale, scp, at, row = out[row:row + samples], at, at + step, row + samples
+        if each[2]:
+            dshift, shp, at, row = out[row:row + samples], at, at + step, row + samples
+        if whole[0]:
+            dpre, prp, at, row = out[row], at, at + 4 * c, row + 1
+        if whole[1]:
+            dpost, pop = out[row], at
     need = _lib.tern_residual_norm_bwd_workspace(args)
     workspace = r_out.new_empty(need, dtype=torch.uint8)
     _check("tern_residual_norm_bwd", _lib.tern_residual_norm_bwd(

@@ -24,7 +24,8 @@
 // The maximum is only raised when a row's new one exceeds it by more than 8 in
 // log2 (so exp2 stays below 256 and the sum exact to fp32): after the first
 // tiles the accumulators are hardly ever rescaled.  P is rounded to bf16 for
-// the product with v (the type of every operand of the matrix cores here); S,
+// the product with v (the type of every operand of the matrix cores here), in small
+// calls with what that left over as a second operand (in_two_operands); S,
 // the maximum, the sum and the accumulators are fp32.
 // Rows of masked keys arrive in LDS as zeros, so what memory holds there (a NaN in
 // padding) does not count; tiles without a kept key are skipped.
@@ -36,7 +37,7 @@ namespace {
 [[maybe_unused]] constexpr float kLn2 = 0.6931471805599453f;
 [[maybe_unused]] constexpr float kRaise = 8.0f;
 
-template <int CPR, int RW, int KW, bool MASK>
+template <int CPR, int RW, int KW, bool MASK, bool TWO>
 __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kernel(
     AttentionParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
         for (int e = 0; e < 16; ++e) o[d][e] *= a;
     }
     const float shift = m == -INFINITY ? 0.0f : m * p.scale_log2;
-    bf16x8_t pf[2 * kSub];
+    bf16x8_t pf[2 * kSub], rest[TWO ? 2 * kSub : 1];
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
       float x[16];
@@ -193,12 +194,19 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
       }
       pf[2 * u] = to_operand(x);
       pf[2 * u + 1] = to_operand(x + 8);
+      if constexpr (TWO) {
+        rest[2 * u] = rest_operand(x, pf[2 * u]);
+        rest[2 * u + 1] = rest_operand(x + 8, pf[2 * u + 1]);
+      }
     }
 #pragma unroll
     for (int c = 0; c < 2 * kSub; ++c)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        o[d] = mfma32(turned.read(vl, d, c), pf[c], o[d]);
+      for (int d = 0; d < DT; ++d) {
+        const bf16x8_t vt = turned.read(vl, d, c);
+        o[d] = mfma32(vt, pf[c], o[d]);
+        if constexpr (TWO) o[d] = mfma32(vt, rest[c], o[d]);
+      }
   };
 
   int t = next_tile(t_first);
@@ -470,21 +478,28 @@ Plan plan(const AttentionParams& p) {
   return r;
 }
 
-template <int CPR>
-hipError_t launch(const AttentionParams& p, bool few, int64_t grid, hipStream_t stream) {
-  const dim3 g(static_cast<unsigned>(grid)), b(256);
-  if (few) {
-    if (p.mask)
-      hipLaunchKernelGGL((attention_kernel<CPR, 1, 4, true>), g, b, 0, stream, p);
+template <int CPR, int RW, int KW>
+hipError_t launch_form(const AttentionParams& p, bool two, int64_t grid, hipStream_t stream) {
+  const dim3 g(static_cast<unsigned>(grid)), b(64 * RW * KW);
+  if (p.mask) {
+    if (two)
+      hipLaunchKernelGGL((attention_kernel<CPR, RW, KW, true, true>), g, b, 0, stream, p);
     else
-      hipLaunchKernelGGL((attention_kernel<CPR, 1, 4, false>), g, b, 0, stream, p);
+      hipLaunchKernelGGL((attention_kernel<CPR, RW, KW, true, false>), g, b, 0, stream, p);
   } else {
-    if (p.mask)
-      hipLaunchKernelGGL((attention_kernel<CPR, 4, 1, true>), g, b, 0, stream, p);
+    if (two)
+      hipLaunchKernelGGL((attention_kernel<CPR, RW, KW, false, true>), g, b, 0, stream, p);
     else
-      hipLaunchKernelGGL((attention_kernel<CPR, 4, 1, false>), g, b, 0, stream, p);
+      hipLaunchKernelGGL((attention_kernel<CPR, RW, KW, false, false>), g, b, 0, stream, p);
   }
   return hipGetLastError();
+}
+
+template <int CPR>
+hipError_t launch(const AttentionParams& p, bool few, int64_t grid, hipStream_t stream) {
+  const bool two = in_two_operands(p.b, p.hkv, p.rows, p.sk, p.d);
+  return few ? launch_form<CPR, 1, 4>(p, two, grid, stream)
+             : launch_form<CPR, 4, 1>(p, two, grid, stream);
 }
 
 }  // namespace

@@ -19,7 +19,8 @@
 // stay in its column, which is not stored.
 // Where there are too few workgroups, the loop is split among several, whose
 // fp32 sums a last kernel adds in order.
-// P and dS are rounded to bf16 as operands; S, dP, delta and all sums are fp32.
+// P and dS are rounded to bf16 as operands, in small calls with what that left over as
+// second ones (in_two_operands); S, dP, delta and all sums are fp32.
 #include "attention_common.h"
 
 namespace tern {
@@ -68,7 +69,7 @@ __device__ inline void store_f32(const f32x16_t (&acc)[DT], float factor, float*
     }
 }
 
-template <int CPR, bool MASK>
+template <int CPR, bool MASK, bool TWO>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = 4, BK = 64, DS = CPR / 2, DT = (CPR + 3) / 4;
@@ -195,10 +196,16 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const bf16x8_t ds = to_operand(x + 8 * c);
+        bf16x8_t rest;
+        if constexpr (TWO) rest = rest_operand(x + 8 * c, ds);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          dq[d] = mfma32(turned.read(kl, d, 2 * u + c), ds, dq[d]);
+        for (int d = 0; d < DT; ++d) {
+          const bf16x8_t kt = turned.read(kl, d, 2 * u + c);
+          dq[d] = mfma32(kt, ds, dq[d]);
+          if constexpr (TWO) dq[d] = mfma32(kt, rest, dq[d]);
+        }
       }
+      phase_end();
     }
   };
 
@@ -232,8 +239,8 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-template <int CPR, bool MASK>
-__global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttentionBwdParams p) {
+template <int CPR, bool MASK, bool TWO>
+__global__ __launch_bounds__(256, TWO ? 1 : 2) void attention_dkv_kernel(AttentionBwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = 4, BR = kRowTile, BK = 32 * NW, DS = CPR / 2, DT = (CPR + 3) / 4;
   constexpr bool kValuesInLds = CPR > 10;
@@ -365,10 +372,19 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttentionBwdParam
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const bf16x8_t pf = to_operand(x + 8 * c), df = to_operand(y + 8 * c);
+        bf16x8_t prest, drest;
+        if constexpr (TWO) {
+          prest = rest_operand(x + 8 * c, pf);
+          drest = rest_operand(y + 8 * c, df);
+        }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          dv[d] = mfma32(turned.read(ol, d, 2 * u + c), pf, dv[d]);
-          dk[d] = mfma32(turned.read(ql, d, 2 * u + c), df, dk[d]);
+          const bf16x8_t ot = turned.read(ol, d, 2 * u + c);
+          dv[d] = mfma32(ot, pf, dv[d]);
+          if constexpr (TWO) dv[d] = mfma32(ot, prest, dv[d]);
+          const bf16x8_t qt = turned.read(ql, d, 2 * u + c);
+          dk[d] = mfma32(qt, df, dk[d]);
+          if constexpr (TWO) dk[d] = mfma32(qt, drest, dk[d]);
         }
       }
     }
@@ -478,29 +494,33 @@ BwdPlan plan(const AttentionBwdParams& p) {
   return r;
 }
 
+template <int CPR, bool MASK, bool TWO>
+hipError_t launch_kernels(const AttentionBwdParams& p, int64_t by_rows, int64_t by_keys,
+                          hipStream_t stream) {
+  if (by_rows > 0) {
+    hipLaunchKernelGGL((attention_dq_kernel<CPR, MASK, TWO>), dim3(static_cast<unsigned>(by_rows)),
+                       dim3(256), 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (by_keys > 0)
+    hipLaunchKernelGGL((attention_dkv_kernel<CPR, MASK, TWO>), dim3(static_cast<unsigned>(by_keys)),
+                       dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
 template <int CPR>
 hipError_t launch(const AttentionBwdParams& p, hipStream_t stream) {
   const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
   const int64_t by_rows = bh * p.row_blocks * p.dq_splits;
   const int64_t by_keys = bh * p.key_blocks * p.dkv_splits;
   if (by_rows > 0x7FFFFFFF || by_keys > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (by_rows > 0) {
-    const dim3 g(static_cast<unsigned>(by_rows));
-    if (p.mask)
-      hipLaunchKernelGGL((attention_dq_kernel<CPR, true>), g, dim3(256), 0, stream, p);
-    else
-      hipLaunchKernelGGL((attention_dq_kernel<CPR, false>), g, dim3(256), 0, stream, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (by_keys > 0) {
-    const dim3 g(static_cast<unsigned>(by_keys));
-    if (p.mask)
-      hipLaunchKernelGGL((attention_dkv_kernel<CPR, true>), g, dim3(256), 0, stream, p);
-    else
-      hipLaunchKernelGGL((attention_dkv_kernel<CPR, false>), g, dim3(256), 0, stream, p);
-  }
-  return hipGetLastError();
+  const bool two = in_two_operands(p.b, p.hkv, p.rows, p.sk, p.d);
+  if (p.mask)
+    return two ? launch_kernels<CPR, true, true>(p, by_rows, by_keys, stream)
+               : launch_kernels<CPR, true, false>(p, by_rows, by_keys, stream);
+  return two ? launch_kernels<CPR, false, true>(p, by_rows, by_keys, stream)
+             : launch_kernels<CPR, false, false>(p, by_rows, by_keys, stream);
 }
 
 hipError_t add(const Sums& a, const Sums& b, int gradients, int splits, int hkv, int group,
