@@ -380,25 +380,27 @@ __global__ __launch_bounds__(NCH == 1 ? 768 : 512) void residual_norm_bwd_kernel
   for (int64_t start = row0; start < row1;) {
     const int64_t sample = start / p.tokens;
     const int64_t end = (sample + 1) * p.tokens < row1 ? (sample + 1) * p.tokens : row1;
-    float gate[NCH][8], scale[NCH][8], wpre[NCH][8], wpost[NCH][8];
+    // Every slot takes part in every barrier; a slot past the end repeats the
+    // last row without adding or writing it.
+    fetch(start + slot < end ? start + slot : end - 1);
+    // Of the sample: alpha gate w_post and (1 + scale) w_pre.
+    float gate[NCH][8], scale[NCH][8];
     float sum_n[NCH][8], sum_z[NCH][8], sum_h[NCH][8];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      load_vector<WIDE>(p.pre_weight, wpre[j], 1.0f, j, n, lane, c);
-      load_vector<WIDE>(p.post_weight, wpost[j], 1.0f, j, n, lane, c);
+      float w[8];
       load_vector<WIDE>(p.gate ? p.gate + sample * p.ldgate : nullptr, gate[j], 1.0f, j, n, lane, c);
       load_vector<WIDE>(p.scale ? p.scale + sample * p.ldscale : nullptr, scale[j], 0.0f, j, n, lane, c);
+      load_vector<WIDE>(p.post_weight, w, 1.0f, j, n, lane, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gate[j][e] *= p.residual_scale * w[e];
+      load_vector<WIDE>(p.pre_weight, w, 1.0f, j, n, lane, c);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        gate[j][e] *= p.residual_scale;
-        scale[j][e] = (1.0f + scale[j][e]) * wpre[j][e];
+        scale[j][e] = (1.0f + scale[j][e]) * w[e];
         sum_n[j][e] = sum_z[j][e] = sum_h[j][e] = 0.0f;
       }
     }
-    // Every slot takes part in every barrier; a slot past the end repeats the
-    // last row without adding or writing it.
-    if (start + slot < end) fetch(start + slot);
-    else fetch(end - 1);
     for (int64_t first = start; first < end; first += p.slots) {
       const int64_t row = first + slot;
       const bool live = row < end;
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(NCH == 1 ? 768 : 512) void residual_norm_bwd_kernel
             const bool in = inside<WIDE>(j, e, n, lane, c);
             if (!in) dr[j][e] = 0.0f;
             if (p.post != TERN_NORM_NONE) z[j][e] = in ? (z[j][e] - st.z) * st.w : 0.0f;
-            g[j][e] = gate[j][e] * wpost[j][e] * dr[j][e];
+            g[j][e] = gate[j][e] * dr[j][e];
             if (live) sum_z[j][e] = __builtin_fmaf(dr[j][e], z[j][e], sum_z[j][e]);
           }
         if (p.post != TERN_NORM_NONE)
