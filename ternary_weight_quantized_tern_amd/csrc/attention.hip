@@ -135,8 +135,11 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
 #pragma unroll
   for (int t = 0; t < DT; ++t) o[t] = f32x16_t{};
   float m = -INFINITY, l = 0.0f;
+  // A wave without a live row only copies and meets.
+  const bool busy = (block * RW + rw) * 32 < p.rows;
 
   auto compute = [&](int t, const uint8_t* kl, const uint8_t* vl) {
+    if (!busy) return;
     by_row.pin();
     turned.pin();
     f32x16_t s[kSub];
@@ -262,8 +265,9 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
     l = lo + hi;
   }
   if constexpr (KW == 1) {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const float lse2 = l > 0.0f ? __builtin_fmaf(m, p.scale_log2, __builtin_amdgcn_logf(l)) : -INFINITY;
+    // (l is 0 where no key is kept; a NaN passes on into o and lse.)
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float lse2 = l == 0.0f ? -INFINITY : __builtin_fmaf(m, p.scale_log2, __builtin_amdgcn_logf(l));
     if (p.splits > 1) {
       const int64_t r = (static_cast<int64_t>(split) * p.b * p.hkv + bh) * p.rows + row;
       if (pr.live) {
@@ -319,9 +323,9 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
 #pragma unroll
     for (int w = 0; w < KW; ++w) {
       const float2 j = joined[w][i];
-      if (j.y > 0.0f) total += j.y * __builtin_amdgcn_exp2f((j.x - top) * p.scale_log2);
+      if (j.y != 0.0f) total += j.y * __builtin_amdgcn_exp2f((j.x - top) * p.scale_log2);
     }
-    const float inv = total > 0.0f ? mine / total : 0.0f;
+    const float inv = total == 0.0f ? 0.0f : mine / total;
     // [32 rows][32 DT channels] of each wave, in the tiles' buffers; rows a bank apart.
     constexpr int kPitch = 32 * DT + 4;
     float* parts[4] = {reinterpret_cast<float*>(k0), reinterpret_cast<float*>(k1),
@@ -339,7 +343,7 @@ __global__ __launch_bounds__(64 * RW * KW, KW == 1 ? 2 : 1) void attention_kerne
     }
     __syncthreads();
     const float lse2 =
-        total > 0.0f ? __builtin_fmaf(top, p.scale_log2, __builtin_amdgcn_logf(total)) : -INFINITY;
+        total == 0.0f ? -INFINITY : __builtin_fmaf(top, p.scale_log2, __builtin_amdgcn_logf(total));
     const int head = hk * p.group + pr.head;
     const int64_t part_row = (static_cast<int64_t>(split) * p.b * p.hkv + bh) * p.rows;
     if (wave == 0 && h == 0 && pr.live) {
@@ -399,21 +403,20 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
       }
     }
     const float to = fmaxf(fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])), top);
-    if (to > -INFINITY) {
-      const float old = __builtin_amdgcn_exp2f(top - to);
-      top = to;
-      total *= old;
+    const float from = to == -INFINITY ? 0.0f : to;
+    const float old = __builtin_amdgcn_exp2f(top - from);
+    top = to;
+    total *= old;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] *= old;
+    for (int e = 0; e < 8; ++e) sum[e] *= old;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float w = __builtin_amdgcn_exp2f(lse[x] - top);
-        total += w;
+    for (int x = 0; x < 4; ++x) {
+      const float w = __builtin_amdgcn_exp2f(lse[x] - from);
+      total += w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum[e] = __builtin_fmaf(w, a[x][e], sum[e]);
-          sum[4 + e] = __builtin_fmaf(w, b[x][e], sum[4 + e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        sum[e] = __builtin_fmaf(w, a[x][e], sum[e]);
+        sum[4 + e] = __builtin_fmaf(w, b[x][e], sum[4 + e]);
       }
     }
   }
@@ -424,7 +427,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
   total *= mine;
   total += __shfl_xor(total, 16);
   total += __shfl_xor(total, 32);
-  const float share = total > 0.0f ? mine / total : 0.0f;
+  const float share = total == 0.0f ? 0.0f : mine / total;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     sum[e] *= share;
@@ -441,7 +444,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
                                  static_cast<int64_t>(head) * p.oh + c) = to_operand(sum);
   if (lane == 0 && p.lse != nullptr)
     p.lse[(static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + to.token] =
-        total > 0.0f ? (all + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+        total == 0.0f ? -INFINITY : (all + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 constexpr int kFewRows = 64;

@@ -166,8 +166,11 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttentionBwdParams
   f32x16_t dq[DT];
 #pragma unroll
   for (int t = 0; t < DT; ++t) dq[t] = f32x16_t{};
+  // A wave without a live row only copies and meets.
+  const bool busy = (block * NW + wave) * 32 < p.rows;
 
   auto compute = [&](int t, const uint8_t* kl, const uint8_t* vl) {
+    if (!busy) return;
     const unsigned long long w = word_of(t);
     by_row.pin();
     turned.pin();
@@ -282,6 +285,8 @@ __global__ __launch_bounds__(256, TWO ? 1 : 2) void attention_dkv_kernel(Attenti
     }
   }
   if ((words[0] | words[1]) == 0) t_end = t_first;  // the same in every wave: nothing to add
+  // A wave without a kept key only copies and meets.
+  const bool busy = static_cast<uint32_t>(words[wave >> 1] >> (32 * (wave & 1))) != 0;
   const bool kept = ((words[wave >> 1] >> ((32 * wave + i) & 63)) & 1ull) != 0;
 
   // The keys (and, where registers allow, values) of this lane's column; zeros
@@ -343,6 +348,7 @@ __global__ __launch_bounds__(256, TWO ? 1 : 2) void attention_dkv_kernel(Attenti
   for (int t = 0; t < DT; ++t) dk[t] = dv[t] = f32x16_t{};
 
   auto compute = [&](const uint8_t* ql, const uint8_t* ol, const float* st) {
+    if (!busy) return;
     by_row.pin();
     turned.pin();
 #pragma unroll

@@ -186,6 +186,26 @@ def test_forward_strides_layouts_and_broadcasts(sq):
     assert torch.equal(o, o2)
 
 
+@pytest.mark.parametrize("sk", [40, 3000])
+@pytest.mark.parametrize("sq", [3, 140])
+def test_forward_passes_on_what_kept_keys_hold(sq, sk):
+    """A NaN in a kept key makes its head's rows and their lse NaN, no other's; a
+    sample whose keys are all masked stays at 0 and -inf."""
+    q, k, v, _ = make(2, sq, sk, 4, 4, 64, None, 5)
+    k[0, sk // 2, 1] = math.nan
+    k[1, sk // 2, 1] = math.nan
+    mask = torch.ones(2, sk, dtype=torch.bool, device=DEV)
+    mask[1] = False
+    o, lse = tern.attention(q, k, v, mask=mask)
+    assert o[0, :, 1].isnan().all() and lse[0, 1].isnan().all()
+    assert not o[0, :, [0, 2, 3]].isnan().any() and not lse[0, [0, 2, 3]].isnan().any()
+    assert (o[1] == 0).all() and (lse[1] == -math.inf).all()
+    k[0, :, 1] = math.nan  # no key of the row is a number
+    o, lse = tern.attention(q, k, v, mask=mask)
+    assert o[0, :, 1].isnan().all() and lse[0, 1].isnan().all()
+    assert not o[0, :, [0, 2, 3]].isnan().any() and not lse[0, [0, 2, 3]].isnan().any()
+
+
 def test_forward_without_keys_or_queries():
     q, k, v, _ = make(2, 5, 4, 2, 2, 64, None, seed=1)
     o, lse = tern.attention(q, k[:, :0], v[:, :0])
