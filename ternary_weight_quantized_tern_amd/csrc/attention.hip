@@ -16,7 +16,7 @@
 //  * many rows: four waves of 32 rows each share tiles of 64 keys.  Two
 //    workgroups fit on a CU (two tiles of K and V in LDS each, under 256
 //    registers), so the softmax of one wave runs beside the products of another.
-//  * few rows (at most 64): the four waves take 32 keys each of tiles of 128
+//  * few rows (at most 32): the four waves take 32 keys each of tiles of 128
 //    for the same 32 rows and are joined through LDS at the end: a stream of keys.
 // With too few workgroups for the chip the keys are split among several, whose
 // normalised parts (fp32) and log-sum-exps a second kernel joins.
@@ -447,7 +447,11 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
         total == 0.0f ? -INFINITY : (all + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
-constexpr int kFewRows = 64;
+// Rows up to which the stream form is used: one block of it.  With two blocks the
+// keys are read twice: 33 rows x 2048 keys x 24 heads 16.1 us as two blocks
+// of this form, 14.4 in the other; 64 rows 17.1 and 16.3; 128 rows 23.0 and 19.2.
+// (At 300 keys, too few to split, two blocks are ahead: 64 rows 7.9 and 8.2.)
+constexpr int kFewRows = 32;
 
 struct Plan {
   bool few;
@@ -457,13 +461,21 @@ struct Plan {
 
 // Few rows: split until there is a workgroup for each CU (one fits on it); many
 // rows: two for each.  A part has at least two tiles (few) or four, and with a
-// mask at most what fits its words.
+// mask at most what fits its words.  Measured beside it:
+//  * few, 128, 384 and 512 workgroups in place of 256: one row of 4 x 24 heads, four to
+//    a key-value head, x 4608
+//    keys 20.7, 23.2 and 22.5 us against 17.2;
+//  * many, 256 and 1024 in place of 512: 256 rows x 24 heads x 8192 keys 55 and
+//    65 us against 53, 1024 rows x 4096 keys 82 and 88 against 86;
+//  * at least one tile or four (few): 64 rows x 300 keys 9.9 and 7.9 us against
+//    7.9; at least two or eight (many): 128 rows x 2048 keys 21.3 and 21.9
+//    against 19.3.
 Plan plan(const AttentionParams& p) {
   Plan r;
   r.few = p.rows <= kFewRows;
   const int bk = r.few ? 128 : 64, least = r.few ? 2 : 4;
   const int64_t wanted = r.few ? 256 : 512;
-  r.row_blocks = (p.rows + (r.few ? 31 : 127)) / (r.few ? 32 : 128);
+  r.row_blocks = r.few ? (p.rows > 0) : (p.rows + 127) / 128;
   r.tiles = static_cast<int>((p.sk + bk - 1) / bk);
   const int64_t base = static_cast<int64_t>(p.b) * p.hkv * r.row_blocks;
   int64_t splits = wanted / base;

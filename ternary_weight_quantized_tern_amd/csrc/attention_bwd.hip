@@ -14,8 +14,8 @@
 // registers, K is read from LDS by rows and transposed, V by rows.  It also
 // forms delta and the row's log2-sum-exp for the second kernel.
 // By keys: S = Q k^T and dP = dO v^T put a key in each lane's column, P and dS
-// are the B operands of dv^T = dO^T P and dk^T = Q^T dS; k and v stay in
-// registers, Q and dO are read from LDS by rows and transposed.  Products of a masked key
+// are the B operands of dv^T = dO^T P and dk^T = Q^T dS; k stays in registers and
+// v in LDS, Q and dO are read from LDS by rows and transposed.  Products of a masked key
 // stay in its column, which is not stored.
 // Where there are too few workgroups, the loop is split among several, whose
 // fp32 sums a last kernel adds in order.
@@ -246,13 +246,12 @@ template <int CPR, bool MASK, bool TWO>
 __global__ __launch_bounds__(256, TWO ? 1 : 2) void attention_dkv_kernel(AttentionBwdParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = 4, BR = kRowTile, BK = 32 * NW, DS = CPR / 2, DT = (CPR + 3) / 4;
-  constexpr bool kValuesInLds = CPR > 10;
   constexpr uint32_t kBytes = tile_bytes<CPR>(BR);
   __shared__ __attribute__((aligned(1024))) uint8_t q0[kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t q1[kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t o0[kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t o1[kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t values[kValuesInLds ? tile_bytes<CPR>(BK) : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t values[tile_bytes<CPR>(BK)];
   // lse2 and delta of a tile's rows.
   __shared__ __attribute__((aligned(1024))) float st0[2 * 64];
   __shared__ __attribute__((aligned(1024))) float st1[2 * 64];
@@ -289,31 +288,24 @@ __global__ __launch_bounds__(256, TWO ? 1 : 2) void attention_dkv_kernel(Attenti
   const bool busy = static_cast<uint32_t>(words[wave >> 1] >> (32 * (wave & 1))) != 0;
   const bool kept = ((words[wave >> 1] >> ((32 * wave + i) & 63)) & 1ull) != 0;
 
-  // The keys (and, where registers allow, values) of this lane's column; zeros
-  // where they do not count.
-  bf16x8_t kf[DS], vf[kValuesInLds ? 1 : DS];
+  // The keys of this lane's column in registers, the values in LDS (two workgroups
+  // fit on a CU that way); zeros where they do not count.
+  bf16x8_t kf[DS];
   {
     const uint16_t* k = p.k + b * p.kb + hk * p.kh + key * p.kt;
-    const uint16_t* v = p.v + b * p.vb + hk * p.vh + key * p.vt;
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
       const int c = 16 * s + 8 * h;
       kf[s] = bf16x8_t{};
       if (kept && c < p.d) kf[s] = *reinterpret_cast<const bf16x8_t*>(k + c);
-      if constexpr (!kValuesInLds) {
-        vf[s] = bf16x8_t{};
-        if (kept && c < p.d) vf[s] = *reinterpret_cast<const bf16x8_t*>(v + c);
-      }
     }
   }
-  if constexpr (kValuesInLds) {
-    if (t_first < t_end) {
-      TileCopy<CPR, BK, NW> vcopy;
-      vcopy.plan(wave, lane, p.vt, p.d);
-      auto keep = [&](uint32_t r) { return ((words[r >> 6] >> (r & 63u)) & 1ull) != 0; };
-      vcopy.issue(p.v + b * p.vb + hk * p.vh + first_key * p.vt, values, wave, lane,
-                  (words[0] & words[1]) == ~0ull, keep);
-    }
+  if (t_first < t_end) {
+    TileCopy<CPR, BK, NW> vcopy;
+    vcopy.plan(wave, lane, p.vt, p.d);
+    auto keep = [&](uint32_t r) { return ((words[r >> 6] >> (r & 63u)) & 1ull) != 0; };
+    vcopy.issue(p.v + b * p.vb + hk * p.vh + first_key * p.vt, values, wave, lane,
+                (words[0] & words[1]) == ~0ull, keep);
   }
 
   TileCopy<CPR, BR, NW> qcopy, ocopy;
@@ -357,11 +349,10 @@ __global__ __launch_bounds__(256, TWO ? 1 : 2) void attention_dkv_kernel(Attenti
 #pragma unroll
       for (int c = 0; c < DS; ++c) {
         s = mfma32(read_rows(ql + u * (32 * CPR * 16u), by_row.at(c)), kf[c], s);
-        const bf16x8_t v = kValuesInLds ? read_rows(values + wave * (32 * CPR * 16u), by_row.at(c))
-                                        : vf[kValuesInLds ? 0 : c];
+        const bf16x8_t v = read_rows(values + wave * (32 * CPR * 16u), by_row.at(c));
         dp = mfma32(read_rows(ol + u * (32 * CPR * 16u), by_row.at(c)), v, dp);
       }
-      order_reads_ahead<DS, 2, kValuesInLds ? 3 : 2, 2>();
+      order_reads_ahead<DS, 2, 3, 2>();
       phase_end();
       float x[16], y[16];
 #pragma unroll

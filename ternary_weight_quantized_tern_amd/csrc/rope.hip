@@ -16,7 +16,8 @@
 // error through one fma, and only then whole turns are dropped.  The angle
 // is therefore right to about 2^-24 turns for positions up to 2^24, where an fp32
 // product alone would lose a bit for every doubling of the position.
-// 4608 tokens x 48 heads of 128 in bf16 (113 MB): see the figures at the launch.
+// 4608 tokens x 48 heads of 128 in bf16 (113 MB): 20.4 us, 5.6 TB/s, the rate of
+// a plain copy from memory.
 #include "internal.h"
 
 namespace tern {
@@ -134,9 +135,12 @@ hipError_t launch(RopeParams& a, int64_t b, int64_t t, hipStream_t stream) {
   a.turn_units = (a.pairs + VP - 1) / VP;
   a.rest_units = (a.d - 2 * a.pairs + 2 * VP - 1) / (2 * VP);
   const int64_t units = a.turn_units + a.rest_units;
-  // Four heads a thread where that leaves enough threads to fill the chip.
+  // Four heads a thread share a pair's sine and cosine, where that leaves a wave for
+  // each SIMD of the chip (2^16 threads).  Four against one head of 128 a thread:
+  // 4608 x 48 heads 20.4 against 33.7 us, 1024 x 24 4.9 against 5.9 (98 thousand
+  // threads), 512 x 24 4.3 against 4.1 (49 thousand), 256 x 24 4.1 against 3.5.
   const int64_t quarter = (static_cast<int64_t>(a.h) + 3) / 4;
-  const bool four = b * t * units * quarter >= (int64_t(1) << 17);
+  const bool four = b * t * units * quarter >= (int64_t(1) << 16);
   a.lanes = static_cast<uint32_t>(four ? quarter : a.h);
   a.items = static_cast<uint32_t>(t * units * a.lanes);
   const dim3 grid((a.items + 255u) / 256u, static_cast<unsigned>(b));
