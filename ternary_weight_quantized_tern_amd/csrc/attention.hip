@@ -447,43 +447,38 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
         total == 0.0f ? -INFINITY : (all + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
-// Rows up to which the stream form is used: one block of it.  With two blocks the
-// keys are read twice: 33 rows x 2048 keys x 24 heads 16.1 us as two blocks
-// of this form, 14.4 in the other; 64 rows 17.1 and 16.3; 128 rows 23.0 and 19.2.
-// (At 300 keys, too few to split, two blocks are ahead: 64 rows 7.9 and 8.2.)
-constexpr int kFewRows = 32;
-
 struct Plan {
   bool few;
   int tiles, tiles_per_split, splits, row_blocks;
   int64_t part_bytes;
 };
 
-// Few rows: split until there is a workgroup for each CU (one fits on it); many
-// rows: two for each.  A part has at least two tiles (few) or four, and with a
-// mask at most what fits its words.  Measured beside it:
-//  * few, 128, 384 and 512 workgroups in place of 256: one row of 4 x 24 heads, four to
-//    a key-value head, x 4608
-//    keys 20.7, 23.2 and 22.5 us against 17.2;
-//  * many, 256 and 1024 in place of 512: 256 rows x 24 heads x 8192 keys 55 and
-//    65 us against 53, 1024 rows x 4096 keys 82 and 88 against 86;
-//  * at least one tile or four (few): 64 rows x 300 keys 9.9 and 7.9 us against
-//    7.9; at least two or eight (many): 128 rows x 2048 keys 21.3 and 21.9
-//    against 19.3.
+// Few rows (kFewRows): one block of the stream form.  With two blocks the keys are
+// read twice: 33 rows x 2048 keys x 24 heads 16.1 us as two blocks, 14.4 in the
+// other form; 64 rows 17.1 and 16.3; 128 rows 23.0 and 19.2.  (At 300 keys, too
+// few to split, two blocks are ahead: 64 rows 7.9 and 8.2.)  Its parts: stream_splits.
+// Many rows: split until there are two workgroups for each CU, a part has at least
+// four tiles, and with a mask at most what fits its words.  Measured beside it, 256
+// and 1024 workgroups in place of 512: 256 rows x 24 heads x 8192 keys 55 and
+// 65 us against 53, 1024 rows x 4096 keys 82 and 88 against 86; at least two or
+// eight tiles: 128 rows x 2048 keys 21.3 and 21.9 us against 19.3.
 Plan plan(const AttentionParams& p) {
   Plan r;
   r.few = p.rows <= kFewRows;
-  const int bk = r.few ? 128 : 64, least = r.few ? 2 : 4;
-  const int64_t wanted = r.few ? 256 : 512;
+  const int bk = r.few ? kStreamKeys : 64;
   r.row_blocks = r.few ? (p.rows > 0) : (p.rows + 127) / 128;
   r.tiles = static_cast<int>((p.sk + bk - 1) / bk);
   const int64_t base = static_cast<int64_t>(p.b) * p.hkv * r.row_blocks;
-  int64_t splits = wanted / base;
-  if (splits > r.tiles / least) splits = r.tiles / least;
-  if (splits < 1) splits = 1;
-  const int most = p.mask ? kMaskWords * 64 / bk : 1 << 30;
-  const int64_t forced = (static_cast<int64_t>(r.tiles) + most - 1) / most;
-  if (splits < forced) splits = forced;
+  int64_t splits;
+  if (r.few) {
+    splits = stream_splits(r.tiles, base, p.mask != nullptr);
+  } else {
+    splits = 512 / base;
+    if (splits > r.tiles / 4) splits = r.tiles / 4;
+    if (splits < 1) splits = 1;
+    const int64_t forced = (static_cast<int64_t>(r.tiles) + kMaskWords - 1) / kMaskWords;
+    if (p.mask && splits < forced) splits = forced;
+  }
   r.tiles_per_split = static_cast<int>((r.tiles + splits - 1) / splits);
   if (r.tiles_per_split < 1) r.tiles_per_split = 1;
   r.splits = (r.tiles + r.tiles_per_split - 1) / r.tiles_per_split;

@@ -419,6 +419,277 @@ __global__ __launch_bounds__(256, TWO ? 1 : 2) void attention_dkv_kernel(Attenti
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+// All three gradients of a stream of keys for at most kFewRows rows (of the heads
+// that share a key-value head): K and V are read once, where the two kernels above
+// read them twice and each works on a tile that is mostly empty.
+// The four waves take 32 keys each of a tile of 128, two tiles on their way, as the
+// forward stream.  Every product of S and dP is taken both ways from the same operands:
+// keys down for dq^T += K^T dS^T (summed over the waves and the splits at the end), rows
+// down for dv^T = dO^T P and dk^T = Q^T dS, complete for the tile's keys.  The extra
+// matrix work is far below the time the keys take to arrive.
+template <int CPR, bool MASK, bool TWO>
+__global__ __launch_bounds__(256, 1) void attention_bwd_few_kernel(AttentionBwdParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = 4, BK = kStreamKeys, DS = CPR / 2, DT = (CPR + 3) / 4;
+  constexpr uint32_t kBytes = tile_bytes<CPR>(BK), kRows = tile_bytes<CPR>(kFewRows);
+  __shared__ __attribute__((aligned(1024))) uint8_t k0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t k1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t v0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t v1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t ql[kRows];
+  __shared__ __attribute__((aligned(1024))) uint8_t ol[kRows];
+  __shared__ __attribute__((aligned(16))) float stats[2][kFewRows];  // lse2 and delta
+  __shared__ unsigned long long words[MASK ? kMaskWords : 1];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 31, h = lane >> 5;
+
+  const uint32_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int split = at % p.dq_splits;
+  const uint32_t bh = at / p.dq_splits;
+  const int hk = bh % p.hkv, b = bh / p.hkv;
+  const int t_first = split * p.key_tiles_per_split;
+  const int t_end = t_first + p.key_tiles_per_split < p.key_tiles ? t_first + p.key_tiles_per_split
+                                                                  : p.key_tiles;
+  if (MASK) {
+    mask_words(words, p.mask + b * p.ldmask, static_cast<int64_t>(t_first) * BK, p.sk,
+               2 * (t_end - t_first), wave, NW, lane);
+    __syncthreads();
+  }
+
+  const uint16_t* kbase = p.k + b * p.kb + hk * p.kh;
+  const uint16_t* vbase = p.v + b * p.vb + hk * p.vh;
+  TileCopy<CPR, BK, NW> kcopy, vcopy;
+  kcopy.plan(wave, lane, p.kt, p.d);
+  vcopy.plan(wave, lane, p.vt, p.d);
+  auto word_of = [&](int t, int w) -> unsigned long long {
+    if (MASK) return uniform64(words[(t - t_first) * 2 + w]);
+    return tail_word(static_cast<int64_t>(t) * BK + 64 * w, p.sk);
+  };
+  auto issue = [&](int t, uint8_t* kl, uint8_t* vl) {
+    const unsigned long long w0 = word_of(t, 0), w1 = word_of(t, 1);
+    auto keep = [&](uint32_t r) { return (((r >= 64 ? w1 : w0) >> (r & 63u)) & 1ull) != 0; };
+    const bool all = (w0 & w1) == ~0ull;
+    kcopy.issue(kbase + static_cast<int64_t>(t) * BK * p.kt, kl, wave, lane, all, keep);
+    vcopy.issue(vbase + static_cast<int64_t>(t) * BK * p.vt, vl, wave, lane, all, keep);
+  };
+
+  // The rows of this lane's column; q and do go to LDS too, for the transposing reads.
+  const PackedRow pr = packed_row(i, p.rows, p.sq);
+  const int head = hk * p.group + pr.head;
+  bf16x8_t qf[DS], dof[DS];
+  float delta = 0.0f, lse2 = INFINITY;
+  {
+    const uint16_t* q = p.q + b * p.qb + static_cast<int64_t>(pr.token) * p.qt +
+                        static_cast<int64_t>(head) * p.qh;
+    const uint16_t* dout = p.dout + b * p.dob + static_cast<int64_t>(pr.token) * p.dot +
+                           static_cast<int64_t>(head) * p.doh;
+    const uint16_t* o = p.o + b * p.ob + static_cast<int64_t>(pr.token) * p.ot +
+                        static_cast<int64_t>(head) * p.oh;
+    bf16x8_t of[DS];
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const int c = 16 * s + 8 * h;
+      qf[s] = dof[s] = of[s] = bf16x8_t{};
+      if (pr.live && c < p.d) {
+        qf[s] = *reinterpret_cast<const bf16x8_t*>(q + c);
+        dof[s] = *reinterpret_cast<const bf16x8_t*>(dout + c);
+        of[s] = *reinterpret_cast<const bf16x8_t*>(o + c);
+      }
+    }
+    if (pr.live) {
+      lse2 = p.lse[(static_cast<int64_t>(b) * p.hkv * p.group + head) * p.sq + pr.token] * kLog2e;
+      if (lse2 == -INFINITY) lse2 = INFINITY;  // a row without keys: P = 0
+    }
+    // The first tiles set out before anything waits for the rows.
+    if (t_first < t_end) issue(t_first, k0, v0);
+    if (t_first + 1 < t_end) issue(t_first + 1, k1, v1);
+#pragma unroll
+    for (int s = 0; s < DS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        delta = __builtin_fmaf(static_cast<float>(dof[s][e]), static_cast<float>(of[s][e]), delta);
+    float lo, hi;
+    halves(delta, lo, hi);
+    delta = lo + hi;
+    if (wave == 0) {
+#pragma unroll
+      for (int s = 0; s < DS; ++s)
+        *reinterpret_cast<bf16x8_t*>(ql + tile_offset<CPR>(i, 2 * s + h)) = qf[s];
+    } else if (wave == 1) {
+#pragma unroll
+      for (int s = 0; s < DS; ++s)
+        *reinterpret_cast<bf16x8_t*>(ol + tile_offset<CPR>(i, 2 * s + h)) = dof[s];
+    } else if (wave == 2 && h == 0) {
+      stats[0][i] = lse2;
+      stats[1][i] = delta;
+    }
+  }
+
+  RowReads<CPR> by_row;
+  by_row.plan(32 * wave, i, h);
+  TransposedReads<CPR> keys_turned, rows_turned;
+  keys_turned.plan(32 * wave, lane);
+  rows_turned.plan(0, lane);
+
+  f32x16_t dq[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dq[t] = f32x16_t{};
+
+  auto compute = [&](int t, const uint8_t* kl, const uint8_t* vl) {
+    const int64_t key = static_cast<int64_t>(t) * BK + 32 * wave + i;
+    uint16_t* dk_out = p.dk + b * p.dkb + key * p.dkt + hk * p.dkh;
+    uint16_t* dv_out = p.dv + b * p.dvb + key * p.dvt + hk * p.dvh;
+    const uint32_t part = static_cast<uint32_t>(word_of(t, wave >> 1) >> (32 * (wave & 1)));
+    if (part == 0) {  // no kept key in the wave's share
+      const f32x16_t none[DT] = {};
+      store_bf16<DT>(none, 0.0f, dk_out, h, p.d, key < p.sk);
+      store_bf16<DT>(none, 0.0f, dv_out, h, p.d, key < p.sk);
+      return;
+    }
+    by_row.pin();
+    keys_turned.pin();
+    rows_turned.pin();
+    // sk, dpk: keys down; sr, dpr: rows down.
+    f32x16_t sk = f32x16_t{}, dpk = f32x16_t{}, sr = f32x16_t{}, dpr = f32x16_t{};
+#pragma unroll
+    for (int c = 0; c < DS; ++c) {
+      const bf16x8_t kf = read_rows(kl, by_row.at(c)), vf = read_rows(vl, by_row.at(c));
+      sk = mfma32(kf, qf[c], sk);
+      dpk = mfma32(vf, dof[c], dpk);
+      sr = mfma32(qf[c], kf, sr);
+      dpr = mfma32(dof[c], vf, dpr);
+    }
+    order_reads_ahead<DS, 4, 2, 2>();
+    phase_end();
+    {
+      float x[16];
+      const uint32_t mine = part >> (4 * h);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sk[e], p.scale_log2, -lse2)) *
+               (dpk[e] - delta);
+        x[e] = __uint_as_float(__float_as_uint(x[e]) & spread_bit(mine, (e & 3) + 8 * (e >> 2)));
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8_t ds = to_operand(x + 8 * c);
+        bf16x8_t rest;
+        if constexpr (TWO) rest = rest_operand(x + 8 * c, ds);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const bf16x8_t kt = keys_turned.read(kl, d, c);
+          dq[d] = mfma32(kt, ds, dq[d]);
+          if constexpr (TWO) dq[d] = mfma32(kt, rest, dq[d]);
+        }
+      }
+    }
+    phase_end();
+    const bool kept = ((part >> i) & 1u) != 0;
+    f32x16_t dk[DT], dv[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) dk[d] = dv[d] = f32x16_t{};
+    float x[16], y[16];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4_t l = *reinterpret_cast<const f32x4_t*>(&stats[0][8 * g + 4 * h]);
+      const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(&stats[1][8 * g + 4 * h]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 4 * g + e;
+        x[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sr[r], p.scale_log2, -l[e]));
+        y[r] = x[r] * (dpr[r] - dl[e]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const bf16x8_t pf = to_operand(x + 8 * c), df = to_operand(y + 8 * c);
+      bf16x8_t prest, drest;
+      if constexpr (TWO) {
+        prest = rest_operand(x + 8 * c, pf);
+        drest = rest_operand(y + 8 * c, df);
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const bf16x8_t ot = rows_turned.read(ol, d, c);
+        dv[d] = mfma32(ot, pf, dv[d]);
+        if constexpr (TWO) dv[d] = mfma32(ot, prest, dv[d]);
+        const bf16x8_t qt = rows_turned.read(ql, d, c);
+        dk[d] = mfma32(qt, df, dk[d]);
+        if constexpr (TWO) dk[d] = mfma32(qt, drest, dk[d]);
+      }
+    }
+    if (!kept) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) dk[d] = dv[d] = f32x16_t{};
+    }
+    store_bf16<DT>(dk, p.scale, dk_out, h, p.d, key < p.sk);
+    store_bf16<DT>(dv, 1.0f, dv_out, h, p.d, key < p.sk);
+  };
+
+  tile_barrier();  // q, do and their statistics are in LDS
+  constexpr int kTile = 2 * TileCopy<CPR, BK, NW>::kOwn;
+  static_assert(TileCopy<CPR, BK, NW>::kInstr % NW == 0, "each wave issues the same copies");
+  int t = t_first;
+  auto use = [&](uint8_t* kl, uint8_t* vl) {
+    // The next tile's copies are the newest of this wave's memory operations (the
+    // stores of the tile before came first): at most they may still be in flight.
+    if (t + 1 < t_end)
+      wait_vmem<kTile>();
+    else
+      wait_vmem();
+    tile_barrier();
+    compute(t, kl, vl);
+    ++t;
+    if (t >= t_end) return false;
+    tile_barrier();
+    if (t + 1 < t_end) issue(t + 1, kl, vl);
+    return true;
+  };
+  if (t < t_end)
+    while (use(k0, v0) && use(k1, v1)) {
+    }
+
+  // dq of the four waves, [32 rows][32 DT channels] each in the tiles' buffers, added
+  // in their order.
+  constexpr int kPitch = 32 * DT + 4;
+  static_assert(kBytes >= 32u * kPitch * 4, "a wave's part fits a buffer");
+  float* parts[4] = {reinterpret_cast<float*>(k0), reinterpret_cast<float*>(k1),
+                     reinterpret_cast<float*>(v0), reinterpret_cast<float*>(v1)};
+  float* own = wave == 0 ? parts[0] : wave == 1 ? parts[1] : wave == 2 ? parts[2] : parts[3];
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<f32x4_t*>(own + i * kPitch + 32 * d + 8 * g + 4 * h) =
+          f32x4_t{dq[d][4 * g], dq[d][4 * g + 1], dq[d][4 * g + 2], dq[d][4 * g + 3]};
+  __syncthreads();
+  for (int x = threadIdx.x; x < 32 * CPR; x += 64 * NW) {
+    const int r = x / CPR, c = (x % CPR) * 8;
+    const PackedRow to = packed_row(r, p.rows, p.sq);
+    if (!to.live || c >= p.d) continue;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int off = r * kPitch + c + e;
+      sum[e] = ((parts[0][off] + parts[1][off]) + (parts[2][off] + parts[3][off])) * p.scale;
+    }
+    if (p.dq_splits > 1) {
+      float* out = p.part_dq +
+                   ((static_cast<int64_t>(split) * p.b * p.hkv + bh) * p.rows + r) * p.d + c;
+      *reinterpret_cast<f32x4_t*>(out) = f32x4_t{sum[0], sum[1], sum[2], sum[3]};
+      *reinterpret_cast<f32x4_t*>(out + 4) = f32x4_t{sum[4], sum[5], sum[6], sum[7]};
+    } else {
+      uint16_t* out = p.dq + b * p.dqb + static_cast<int64_t>(to.token) * p.dqt +
+                      static_cast<int64_t>(hk * p.group + to.head) * p.dqh + c;
+      *reinterpret_cast<bf16x8_t*>(out) = to_operand(sum);
+    }
+  }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
 // The splits' sums, added in order: eight channels a thread.  Two gradients of
 // the same sizes (dk and dv) are two rows of workgroups.
 struct Sums {
@@ -454,6 +725,7 @@ __global__ __launch_bounds__(256) void attention_add_kernel(Sums a, Sums b, int 
 }
 
 struct BwdPlan {
+  bool few;
   int row_blocks, key_tiles, key_tiles_per_split, dq_splits;
   int key_blocks, tiles_per_head, row_tiles, row_tiles_per_split, dkv_splits;
   int64_t stats, part_dq, part_dkv;  // floats
@@ -475,6 +747,21 @@ void split(int64_t tiles, int64_t base, int64_t wanted, int least, int64_t most,
 BwdPlan plan(const AttentionBwdParams& p) {
   BwdPlan r;
   const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
+  auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
+  r.few = p.rows > 0 && p.rows <= kFewRows;
+  if (r.few) {
+    r.row_blocks = 1;
+    r.key_tiles = static_cast<int>((p.sk + kStreamKeys - 1) / kStreamKeys);
+    const int64_t splits = stream_splits(r.key_tiles, bh, p.mask != nullptr);
+    const int64_t each = r.key_tiles > 0 ? (r.key_tiles + splits - 1) / splits : 1;
+    r.key_tiles_per_split = static_cast<int>(each);
+    r.dq_splits = r.key_tiles > 0 ? static_cast<int>((r.key_tiles + each - 1) / each) : 1;
+    r.key_blocks = r.tiles_per_head = r.row_tiles = r.row_tiles_per_split = 0;
+    r.dkv_splits = 1;
+    r.stats = r.part_dkv = 0;
+    r.part_dq = r.dq_splits > 1 ? whole(r.dq_splits * bh * p.rows * p.d) : 0;
+    return r;
+  }
   r.row_blocks = (p.rows + 127) / 128;
   r.key_tiles = static_cast<int>((p.sk + 63) / 64);
   split(r.key_tiles, bh * r.row_blocks, 512, 4, p.mask ? kMaskWords : int64_t(1) << 30,
@@ -484,7 +771,6 @@ BwdPlan plan(const AttentionBwdParams& p) {
   r.row_tiles = r.tiles_per_head * p.group;
   split(r.row_tiles, bh * r.key_blocks, 512, 8, int64_t(1) << 30,
         &r.row_tiles_per_split, &r.dkv_splits);
-  auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
   r.stats = whole(bh * p.rows);
   r.part_dq = r.dq_splits > 1 ? whole(r.dq_splits * bh * p.rows * p.d) : 0;
   r.part_dkv = r.dkv_splits > 1 ? whole(r.dkv_splits * bh * p.sk * p.d) : 0;
@@ -506,13 +792,27 @@ hipError_t launch_kernels(const AttentionBwdParams& p, int64_t by_rows, int64_t 
   return hipGetLastError();
 }
 
+template <int CPR, bool MASK, bool TWO>
+hipError_t launch_few(const AttentionBwdParams& p, int64_t grid, hipStream_t stream) {
+  hipLaunchKernelGGL((attention_bwd_few_kernel<CPR, MASK, TWO>), dim3(static_cast<unsigned>(grid)),
+                     dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
 template <int CPR>
-hipError_t launch(const AttentionBwdParams& p, hipStream_t stream) {
+hipError_t launch(const AttentionBwdParams& p, bool few, hipStream_t stream) {
   const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
   const int64_t by_rows = bh * p.row_blocks * p.dq_splits;
   const int64_t by_keys = bh * p.key_blocks * p.dkv_splits;
   if (by_rows > 0x7FFFFFFF || by_keys > 0x7FFFFFFF) return hipErrorInvalidValue;
   const bool two = in_two_operands(p.b, p.hkv, p.rows, p.sk, p.d);
+  if (few && by_rows > 0) {
+    if (p.mask)
+      return two ? launch_few<CPR, true, true>(p, by_rows, stream)
+                 : launch_few<CPR, true, false>(p, by_rows, stream);
+    return two ? launch_few<CPR, false, true>(p, by_rows, stream)
+               : launch_few<CPR, false, false>(p, by_rows, stream);
+  }
   if (p.mask)
     return two ? launch_kernels<CPR, true, true>(p, by_rows, by_keys, stream)
                : launch_kernels<CPR, true, false>(p, by_rows, by_keys, stream);
@@ -553,11 +853,11 @@ hipError_t launch_attention_bwd(AttentionBwdParams& p, void* workspace, hipStrea
   p.part_dq = w + 2 * r.stats;
   p.part_dk = p.part_dq + r.part_dq;
   p.part_dv = p.part_dk + r.part_dkv;
-  hipError_t e = p.d <= 32   ? launch<4>(p, stream)
-                 : p.d <= 64 ? launch<8>(p, stream)
-                 : p.d <= 80 ? launch<10>(p, stream)
-                 : p.d <= 96 ? launch<12>(p, stream)
-                             : launch<16>(p, stream);
+  hipError_t e = p.d <= 32   ? launch<4>(p, r.few, stream)
+                 : p.d <= 64 ? launch<8>(p, r.few, stream)
+                 : p.d <= 80 ? launch<10>(p, r.few, stream)
+                 : p.d <= 96 ? launch<12>(p, r.few, stream)
+                             : launch<16>(p, r.few, stream);
   const int64_t bh = static_cast<int64_t>(p.b) * p.hkv;
   if (e == hipSuccess && r.dq_splits > 1 && p.rows > 0) {
     const Sums dq = {p.part_dq, p.dq, p.dqb, p.dqt, p.dqh};

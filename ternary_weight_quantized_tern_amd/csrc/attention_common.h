@@ -237,6 +237,9 @@ __device__ inline PackedRow packed_row(int row, int rows, int sq) {
   return r;
 }
 
+// Rows up to which a call is a stream of keys: one block of rows, tiles of kStreamKeys.
+constexpr int kFewRows = 32, kStreamKeys = 128;
+
 constexpr int kMaskWords = 1024;  // 64 keys each: the most that one workgroup walks over
 
 // Bits of `words` x 64 keys from key0 on, one word per 64 keys, into LDS.
@@ -259,6 +262,28 @@ __device__ inline unsigned long long uniform64(unsigned long long v) {
 // All ones where bit `bit` is set, else 0.
 __device__ inline uint32_t spread_bit(uint32_t bits, int bit) {
   return static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(bits), bit, 1));
+}
+
+// Parts of a stream of `tiles` tiles for each of `base` (sample, key-value head)
+// pairs, one workgroup to a CU: up to 64 pairs as many as fill the chip once.
+// With more, what ends first when every workgroup takes its tiles and about one
+// more to start and to end, in rounds of 256.  A part has at least two tiles.
+inline int64_t stream_splits(int64_t tiles, int64_t base, bool masked) {
+  int64_t best = base > 64 ? 1 : 256 / (base > 0 ? base : 1);
+  if (base > 64) {
+    int64_t least = INT64_MAX;
+    for (int64_t n = 1; n == 1 || (n * base <= 1024 && 2 * n <= tiles); ++n) {
+      const int64_t cost = (base * n + 255) / 256 * ((tiles + n - 1) / n + 1);
+      if (cost < least) {
+        least = cost;
+        best = n;
+      }
+    }
+  }
+  if (best > tiles / 2) best = tiles / 2;
+  const int64_t most = kMaskWords * 64 / kStreamKeys;  // tiles whose mask words fit
+  if (masked && best < (tiles + most - 1) / most) best = (tiles + most - 1) / most;
+  return best < 1 ? 1 : best;
 }
 
 // Bits of the keys below `keys` among 64 from key0 on.

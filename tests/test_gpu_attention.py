@@ -321,6 +321,42 @@ def test_backward_matches_the_formulas(b, sq, sk, hq, hkv, d, mask):
         assert float(got[2].float()[~m].abs().sum()) == 0
 
 
+FEW = [
+    # rows of the heads that share a key-value head: at most 32
+    (1, 2, 129, 1, 1, 128, None),
+    (2, 1, 127, 12, 3, 96, "random"),
+    (1, 32, 128, 2, 2, 72, None),
+    (2, 7, 700, 16, 4, 80, "random"),       # 28 rows, the last tile ragged
+    (1, 31, 1500, 3, 3, 40, "suffix"),      # whole tiles masked
+    (70, 1, 520, 2, 1, 64, "prefix"),       # more pairs than one round of workgroups
+    (300, 1, 600, 1, 1, 32, None),          # split though there are many pairs
+    (2, 3, 5000, 4, 4, 128, "one"),
+    (1, 5, 900, 2, 2, 64, "none_kept"),
+    (1, 33, 400, 1, 1, 128, "random"),      # one row too many
+]
+
+
+@pytest.mark.parametrize("b,sq,sk,hq,hkv,d,mask", FEW)
+def test_few_rows_match_the_formulas(b, sq, sk, hq, hkv, d, mask):
+    test_forward_matches_the_formula(b, sq, sk, hq, hkv, d, mask)
+    test_backward_matches_the_formulas(b, sq, sk, hq, hkv, d, mask)
+
+
+def test_backward_few_rows_strides_and_long_mask():
+    log("attention_backward few rows, strides, long mask")
+    g = torch.Generator().manual_seed(21)
+    b, sq, sk, h, d = 1, 4, 66000, 2, 40  # more keys than one workgroup's mask words
+    x = torch.randn(b, h, sq, 2 * d, generator=g).to(torch.bfloat16).to(DEV)
+    kv = torch.randn(sk, b, 3 * h, d, generator=g).to(torch.bfloat16).to(DEV)
+    q, do = x[..., :d].transpose(1, 2), x[..., d:].transpose(1, 2)
+    k, v = kv[:, :, :h].transpose(0, 1), kv[:, :, 2 * h:].transpose(0, 1)
+    mask = (torch.rand(b, sk, generator=g) < 0.01).to(DEV)
+    o, lse = tern.attention(q, k, v, mask=mask)
+    got = tern.attention_backward(do, q, k, v, o, lse, mask=mask)
+    torch.cuda.synchronize()
+    check_backward(do, q, k, v, mask, None, o, lse, got, "few rows, strides")
+
+
 @pytest.mark.parametrize("sq", [3, 140])
 def test_backward_ignores_what_masked_keys_hold(sq):
     log(f"attention_backward masked NaN sq={sq}")
