@@ -456,7 +456,9 @@ struct Plan {
 // Few rows (kFewRows): one block of the stream form.  With two blocks the keys are
 // read twice: 33 rows x 2048 keys x 24 heads 16.1 us as two blocks, 14.4 in the
 // other form; 64 rows 17.1 and 16.3; 128 rows 23.0 and 19.2.  (At 300 keys, too
-// few to split, two blocks are ahead: 64 rows 7.9 and 8.2.)  Its parts: stream_splits.
+// few to split, two blocks are ahead: 64 rows 7.9 and 8.2.)  Its parts: stream_splits,
+// from four tiles on (one row of 24 heads x 512 keys in four parts 9.6 us, in two
+// 11.1; 16 rows of 2 x 16 heads x 300 keys, three tiles, in three 8.8, whole 7.9).
 // Many rows: split until there are two workgroups for each CU, a part has at least
 // four tiles, and with a mask at most what fits its words.  Measured beside it, 256
 // and 1024 workgroups in place of 512: 256 rows x 24 heads x 8192 keys 55 and
@@ -471,7 +473,7 @@ Plan plan(const AttentionParams& p) {
   const int64_t base = static_cast<int64_t>(p.b) * p.hkv * r.row_blocks;
   int64_t splits;
   if (r.few) {
-    splits = stream_splits(r.tiles, base, p.mask != nullptr);
+    splits = stream_splits(r.tiles, base, p.mask != nullptr, 4);
   } else {
     splits = 512 / base;
     if (splits > r.tiles / 4) splits = r.tiles / 4;

@@ -752,7 +752,8 @@ BwdPlan plan(const AttentionBwdParams& p) {
   if (r.few) {
     r.row_blocks = 1;
     r.key_tiles = static_cast<int>((p.sk + kStreamKeys - 1) / kStreamKeys);
-    const int64_t splits = stream_splits(r.key_tiles, bh, p.mask != nullptr);
+    // (16 rows of 2 x 16 heads x 300 keys in three parts 12.0 us, whole 15.6.)
+    const int64_t splits = stream_splits(r.key_tiles, bh, p.mask != nullptr, 2);
     const int64_t each = r.key_tiles > 0 ? (r.key_tiles + splits - 1) / splits : 1;
     r.key_tiles_per_split = static_cast<int>(each);
     r.dq_splits = r.key_tiles > 0 ? static_cast<int>((r.key_tiles + each - 1) / each) : 1;
