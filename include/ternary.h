@@ -588,7 +588,8 @@ typedef struct {
  *   S[s] = scale * <q[b][t][j], k[b][s][j']>   over the keys s that mask keeps,
  *   o[b][t][j] = sum_s softmax(S)[s] v[b][s][j'],   lse[b][j][t] = log sum_s exp S[s]
  * with exact bf16 products, fp32 sums and statistics, the probabilities rounded
- * to bf16 for the second product and one rounding of o to bf16.  A row with no
+ * to bf16 for the second product (where batch heads queries keys width <= 2^25, in
+ * two terms: nearly exact) and one rounding of o to bf16.  A row with no
  * kept key gives o = 0 and lse = -inf.  What memory holds at masked keys (NaN, infinities) does
  * not matter.
  *
@@ -621,7 +622,8 @@ tern_status tern_attention(const tern_heads* q, const tern_heads* k, const tern_
  *   dq = scale sum_s dS k,   dk = scale sum_t dS q,   dv = sum_t P do
  * (dk and dv over the query heads of their key-value head too), fp32 sums in
  * an order fixed by the sizes (repeated calls give identical bits), P and dS
- * rounded to bf16 as operands, one rounding of each gradient to bf16.  Gradients of masked
+ * rounded to bf16 as operands (in two terms as above), one rounding of each gradient to
+ * bf16.  Gradients of masked
  * keys are 0.
  *
  *   dout   [batch, queries, heads, width] bf16 gradient of o

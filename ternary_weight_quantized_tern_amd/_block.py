@@ -83,6 +83,11 @@ def _heads(a: torch.Tensor, name: str, dtypes) -> bytes:
     return _heads_struct(a.data_ptr(), sb if b > 1 else 0, st if t > 1 else 0, sh if h > 1 else 0)
 
 
+def _new_heads(a: torch.Tensor, t: int, h: int, d: int) -> bytes:
+    """The tern_heads of a new contiguous [batch, t, h, d] tensor."""
+    return _heads_struct(a.data_ptr(), t * h * d, h * d, d)
+
+
 def _refuse_heads(a, name: str, dtypes):
     if not isinstance(a, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -308,7 +313,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask=None,
     need = _lib.tern_attention_workspace(shape, mp is not None, 0)
     workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     _check("tern_attention", _lib.tern_attention(
-        qs, ks, vs, _heads(o, "o", _BF16), shape, mp, ldmask, lse.data_ptr(),
+        qs, ks, vs, _new_heads(o, s, h, d), shape, mp, ldmask, lse.data_ptr(),
         workspace.data_ptr() if need else None, need, _stream(stream, q)))
     return o, lse
 
@@ -318,7 +323,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                        stream=None):
     """Gradients ``(dq, dk, dv)`` (bf16, contiguous) of ``attention`` from the gradient
     ``dout`` of ``o``, its arguments and its results ``o`` and ``lse``."""
-    views = [_heads(a, n, _BF16) for a, n in ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (o, "o"))]
+    views = (_heads(dout, "dout", _BF16), _heads(q, "q", _BF16), _heads(k, "k", _BF16),
+             _heads(v, "v", _BF16), _heads(o, "o", _BF16))
     b, s, h, d = q.shape
     if dout.shape != q.shape or o.shape != q.shape:
         raise ValueError("dout and o must have the shape of q")
@@ -328,10 +334,12 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     if tuple(lse.shape) != (b, h, s) or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous [{b}, {h}, {s}] tensor")
     mp, ldmask = _key_mask(mask, b, k.shape[1])
-    dq, dk, dv = (a.new_empty(a.shape) for a in (q, k, v))
+    dq, dk, dv = q.new_empty((b, s, h, d)), q.new_empty(k.shape), q.new_empty(k.shape)
     need = _lib.tern_attention_workspace(shape, mp is not None, 1)
-    workspace = q.new_empty(need, dtype=torch.uint8)
+    workspace = q.new_empty(need, dtype=torch.uint8) if need else None
+    sk, hkv = k.shape[1], k.shape[2]
     _check("tern_attention_bwd", _lib.tern_attention_bwd(
-        *views, lse.data_ptr(), *(_heads(a, "gradient", _BF16) for a in (dq, dk, dv)), shape, mp,
-        ldmask, workspace.data_ptr(), need, _stream(stream, q)))
+        *views, lse.data_ptr(), _new_heads(dq, s, h, d), _new_heads(dk, sk, hkv, d),
+        _new_heads(dv, sk, hkv, d), shape, mp, ldmask, workspace.data_ptr() if need else None, need,
+        _stream(stream, q)))
     return dq, dk, dv

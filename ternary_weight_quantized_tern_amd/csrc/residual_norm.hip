@@ -26,6 +26,11 @@
 // gradients are sums of (1 + scale) S and alpha gate Z over samples.  A
 // workgroup writes one partial triple for each sample that it meets, and a second kernel
 // adds them in order.  No atomics: the order is fixed by the sizes.
+//
+// Measured: forward, 4608 x 3072 in bf16 (113 MB) 21-23 us, 5.0-5.4 TB/s (a copy of a
+// gigabyte 5.2); 8 x 1152, 3.6 us, an almost empty launch being 1.7.  Backward, 2 x 2304 x
+// 3072 in bf16 (170 MB) 35 us, 4.9 TB/s, and 5 for the sums; 8 x 256 x 1152 with an
+// fp32 stream, two RMS norms and their weights (43 MB) 15 us and 7.
 #include "internal.h"
 #include "wave.h"
 
@@ -614,7 +619,9 @@ __global__ __launch_bounds__(64 * kSumWaves) void residual_norm_sums_kernel(
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // A row's waves and the channels a lane holds (8 NCH): one piece a lane up to
-// eight waves (4096 channels), then two.
+// eight waves (4096 channels), then two.  Forward with two pieces from 1024 channels
+// on: 4608 x 3072 23.6 us against 22.5, 16384 x 1152 40 against 29, 4096 x 2048 16.7
+// against 13.7.
 int waves_of(int c, int* pieces) {
   const int whole = (c + 511) / 512;  // waves with one piece a lane
   *pieces = whole <= 8 ? 1 : 2;
@@ -628,7 +635,8 @@ struct BwdPlan {
 
 // About one workgroup of up to 12 waves a CU: each leaves a triple of partial
 // sums a channel (12 bytes written and read) for the rows it takes, so fewer
-// workgroups with several rows side by side cost less than many.
+// workgroups with several rows side by side cost less than many: with 512 in place of 256
+// 2 x 2304 x 3072 took 48 us against 42, 8 x 256 x 1152 30 against 24.
 BwdPlan plan_bwd(int64_t m, int64_t c, int64_t tokens) {
   BwdPlan b;
   b.waves = waves_of(static_cast<int>(c), &b.pieces);
@@ -670,7 +678,9 @@ hipError_t launch_residual_norm(ResidualNormParams& p, bool r_is_bf16, hipStream
   const int waves = waves_of(p.c, &pieces);
   p.threads = 64 * waves;
   // Rows a workgroup walks over: enough workgroups for about 24 waves a CU,
-  // at most 8 rows (past that the sample's vectors cost nothing more).
+  // at most 8 rows.  One row a workgroup reads the sample's vectors too often, many leave
+  // too few in flight: 4608 x 3072 22.5 us, with one row 27.6, with a third of the
+  // workgroups and up to 32 rows 24.4; 16384 x 1152 29, 38 and 38.
   int64_t rows = p.m * waves / (256 * 24);
   p.rows = rows < 1 ? 1 : rows > 8 ? 8 : rows;
   const bool wide = p.c % 8 == 0 && p.ldr % 8 == 0 && aligned16(p.r) && p.ldy % 8 == 0 &&
