@@ -165,8 +165,13 @@ def _rows(a, name: str, dtypes, m: int, c: int):
 def _weight(a, name: str, c: int) -> int:
     if a is None:
         return 0
-    _vec(a, name, torch.float32)
-    if a.shape[0] != c:
+    try:
+        fits = a.is_cuda and a.dtype is torch.float32 and a.shape == (c,) and \
+            (c == 1 or a.stride(0) == 1)
+    except (AttributeError, TypeError):
+        fits = False
+    if not fits:
+        _vec(a, name, torch.float32)
         raise ValueError(f"{name} must be [{c}]")
     return a.data_ptr()
 
@@ -250,28 +255,29 @@ def residual_norm_backward(dr_out, dh, r_out: torch.Tensor, y, stats: torch.Tens
     # The sums' tensors are rows of one: an allocation costs more than a view.
     each = (gate is not None and with_y, scale is not None and with_h, with_shift and with_h)
     whole = (pre_weight is not None and with_h, post_weight is not None and with_y)
-    rows = sum(each) * samples + sum(whole)
-    dgate = dscale = dshift = dpre = dpost = gp = scp = shp = prp = pop = None
+    grads, pointers = [None] * 5, [None] * 5
+    have, singles = each.count(True), whole.count(True)
+    rows = have * samples + singles
     if rows:
         out = r_out.new_empty((rows, c), dtype=torch.float32)
-        at, step, row = out.data_ptr(), 4 * c * samples, 0
-        if each[0]:
-            dgate, gp, at, row = out[row:row + samples], at, at + step, row + samples
-        if each[1]:
-            dscale, scp, at, row = out[row:row + samples], at, at + step, row + samples
-        if each[2]:
-            dshift, shp, at, row = out[row:row + samples], at, at + step, row + samples
-        if whole[0]:
-            dpre, prp, at, row = out[row], at, at + 4 * c, row + 1
-        if whole[1]:
-            dpost, pop = out[row], at
+        parts = [out]
+        if have:
+            parts = list(out.split([samples] * have + [singles] * (singles > 0)))
+        if singles:
+            parts[-1:] = parts[-1].unbind(0)
+        at, n = out.data_ptr(), 0
+        for i, there in enumerate(each + whole):
+            if there:
+                grads[i], pointers[i] = parts[n], at
+                at += 4 * c * (samples if i < 3 else 1)
+                n += 1
     need = _lib.tern_residual_norm_bwd_workspace(args)
     workspace = r_out.new_empty(need, dtype=torch.uint8)
     _check("tern_residual_norm_bwd", _lib.tern_residual_norm_bwd(
         args, drop, lddro, dhp, lddh, rp, ldro, yp, ldy, sp, dr.data_ptr(), c,
-        None if dy is None else dy.data_ptr(), c, gp, scp, shp, prp, pop, workspace.data_ptr(), need,
+        None if dy is None else dy.data_ptr(), c, *pointers, workspace.data_ptr(), need,
         _stream(stream, r_out)))
-    return dr, dy, dgate, dscale, dshift, dpre, dpost
+    return (dr, dy, *grads)
 
 
 def _attention_shape(q, k, v, scale) -> bytes:
