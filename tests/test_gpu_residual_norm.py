@@ -174,6 +174,13 @@ def test_forward_and_backward_match_the_formulas(m, c, tokens, dtype, pre, post,
         assert dpost is None
 
 
+@pytest.mark.parametrize("c", [2, 7, 9, 12, 15, 17, 505, 519, 1153, 4097, 4999, 8191])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_widths_that_cut_a_piece(c, dtype):
+    """Rows whose end falls into eight channels of a lane, at odd pitches."""
+    test_forward_and_backward_match_the_formulas(29, c, 10, dtype, "layer", "rms", True, c % 5)
+
+
 def test_parts_left_out():
     log("residual_norm parts")
     m, c, tokens = 70, 264, 35
