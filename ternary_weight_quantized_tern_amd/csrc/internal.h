@@ -182,8 +182,8 @@ struct AttentionBwdParams {
   int64_t sk;
   float scale, scale_log2;
 
-  // By query rows: blocks of 128 rows, tiles of 64 keys.  By keys: blocks of
-  // 128 keys, tiles of 64 rows of one head.
+  // By query rows: blocks of 128 rows, tiles of 64 keys (few rows: one block, tiles of
+  // 128 keys).  By keys: blocks of 128 keys, tiles of 32 rows of one head.
   int32_t row_blocks, key_tiles, key_tiles_per_split, dq_splits;
   int32_t key_blocks, tiles_per_head, row_tiles, row_tiles_per_split, dkv_splits;
   float *lse2, *delta, *part_dq, *part_dk, *part_dv;  // in the workspace
